@@ -287,6 +287,83 @@ w8a8_status w8a8_linear_noalloc(const void *x, int64_t ldx, const void *packed_w
                                 int64_t M, int64_t N, int64_t K,
                                 w8a8_stream_t stream);
 
+/* ---- microscaled 4-bit (MX) layers -------------------------------------------
+ * No counterpart on the pages: the same dynamic layer with both operands in
+ * the 4-bit format of the OCP Microscaling Formats specification v1.0
+ * (MXFP4), for weights that ship in it and for half the bytes of int8.
+ * A block is 32 consecutive elements of a row (the last one of a row may be
+ * 16); it has one scale byte c, standing for 2^(c - 127) (255: NaN), and 32
+ * e2m1 codes: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and, with the code's high bit, their
+ * negatives.
+ *
+ * Quantisation of a block of bf16 values (exact, the same on every run):
+ *   c    = max(floor(log2(amax)) - 2 + 127, 0);  0 for a block of zeros
+ *   code = x * 2^(127 - c), rounded to the nearest e2m1 value (a tie to the
+ *          even code), magnitudes above 6 to 6; a zero keeps its sign
+ *   A block that holds an infinity or a NaN gets c = 255 and codes 0; it makes
+ *   every output of its row NaN.
+ * Product:
+ *   y[m, n] = bf16(act(sum over blocks 2^(ca + cw - 254) sum 32 qa qw + bias))
+ *   with fp32 accumulation on the tensor core and one rounding to bf16 before
+ *   the activation, as in the int8 layers.  The order of the sums depends on
+ *   the shape alone: equal calls give equal bits.
+ *
+ * Both operands are "images": the tensor core's own order, 128-row by
+ * 256-element tiles of 17,408 bytes (codes, then scales).  An image of M rows
+ * is written for those rows only; rows past M in its last tile keep what
+ * they held.  x and weights have the same image, so w8a8_mx4_quant serves for
+ * both.  Shape limits and errors as for the int8 layers (K % 16, K <= 131072,
+ * N % 8); where the output is an image, N % 16 and N <= 131072 too. */
+
+/* Byte size of the image of a [rows, K] matrix. */
+w8a8_status w8a8_mx4_bytes(int64_t rows, int64_t K, size_t *bytes);
+
+/* x (device, bf16 [rows, K], row stride ldx, ldx % 8 == 0) -> image (device,
+ * image_bytes >= w8a8_mx4_bytes).  One pass: 2 bytes read and 17/32 written
+ * an element. */
+w8a8_status w8a8_mx4_quant(const void *x, int64_t rows, int64_t K, int64_t ldx, void *image,
+                           size_t image_bytes, w8a8_stream_t stream);
+
+/* Load time: a checkpoint's codes (device, [rows, K / 2], two to a byte, the
+ * lower k in the low half, 16-byte aligned) and scale bytes (device, [rows,
+ * ceil(K / 32)]) -> image, and back (test and inspection use). */
+w8a8_status w8a8_mx4_pack(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t K,
+                          void *image, size_t image_bytes, w8a8_stream_t stream);
+w8a8_status w8a8_mx4_unpack(const void *image, int64_t rows, int64_t K, uint8_t *codes,
+                            uint8_t *scales, w8a8_stream_t stream);
+
+/* The values that an image stands for: x (device, bf16 [rows, K] dense). */
+w8a8_status w8a8_mx4_dequant(const void *image, int64_t rows, int64_t K, void *x,
+                             w8a8_stream_t stream);
+
+/* y (device, bf16 [M, N]) from the images of [M, K] and [N, K]; bias (device,
+ * bf16 [N]) or NULL; act: a w8a8_act.  workspace: device scratch of ws_bytes
+ * >= w8a8_mx4_scaled_mm_workspace_bytes (NULL where that is 0); its contents
+ * on entry do not matter.  Calls that share one must not overlap. */
+w8a8_status w8a8_mx4_scaled_mm_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t *bytes);
+w8a8_status w8a8_mx4_scaled_mm(const void *a_image, const void *w_image, const void *bias, void *y,
+                               int64_t M, int64_t N, int64_t K, int act, void *workspace,
+                               size_t ws_bytes, w8a8_stream_t stream);
+
+/* The same product, with the image of y in place of y: equal, bit for bit, to
+ * w8a8_mx4_quant of the y of w8a8_mx4_scaled_mm.  The codes are formed in the
+ * epilogue; y does not reach memory.  y_image_bytes >= w8a8_mx4_bytes(M, N). */
+w8a8_status w8a8_mx4_scaled_mm_quant(const void *a_image, const void *w_image, const void *bias,
+                                     void *y_image, size_t y_image_bytes, int64_t M, int64_t N,
+                                     int64_t K, int act, void *workspace, size_t ws_bytes,
+                                     w8a8_stream_t stream);
+
+/* The whole layer: quantisation of x, then the product as a programmatic
+ * dependent of it.  workspace (never NULL): the image of x, then the
+ * product's workspace. */
+w8a8_status w8a8_mx4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t *bytes);
+w8a8_status w8a8_mx4_linear(const void *x, int64_t ldx, const void *w_image, const void *bias, void *y,
+                            int64_t M, int64_t N, int64_t K, int act, void *workspace, size_t ws_bytes,
+                            w8a8_stream_t stream);
+w8a8_status w8a8_mx4_linear_quant(const void *x, int64_t ldx, const void *w_image, const void *bias,
+                                  void *y_image, size_t y_image_bytes, int64_t M, int64_t N, int64_t K,
+                                  int act, void *workspace, size_t ws_bytes, w8a8_stream_t stream);
+
 /* ---- path selection (tests and benchmarks) ---------------------------------
  * 0 = automatic (default); 1 = always the persistent large-M GEMM (automatic
  * tile width); 2 = the small-M weight-streaming kernel (M <= 16 only, else

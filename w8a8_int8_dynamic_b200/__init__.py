@@ -13,3 +13,7 @@ from .binding import (  # noqa: F401
     linear_act_quant_workspace_bytes, linear_workspace_bytes, pack_weight, pack_weight_int32, packed_weight_bytes,
     poll_status, quant_act, quant_act_static, quant_pack_weight, scaled_mm, scaled_mm_i32, scaled_mm_workspace_bytes, selftest_int8_mma_rate, selftest_wait_timeout,
     set_path, unpack_weight)
+from .mx4 import (  # noqa: F401
+    MX4Linear, MX4Tensor, mx4_bytes, mx4_dequant, mx4_linear, mx4_linear_quant,
+    mx4_linear_workspace_bytes, mx4_pack, mx4_quant, mx4_scaled_mm, mx4_scaled_mm_quant,
+    mx4_scaled_mm_workspace_bytes, mx4_unpack)

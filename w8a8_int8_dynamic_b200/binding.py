@@ -70,6 +70,21 @@ _SIGNATURES = {
                                _SZ, _P], ctypes.c_int),
     "w8a8_linear_noalloc_max_bytes": ([], _SZ),
     "w8a8_linear_noalloc": ([_P, _I64, _P, _P, _P, _P, _I64, _I64, _I64, _P], ctypes.c_int),
+    "w8a8_mx4_bytes": ([_I64, _I64, ctypes.POINTER(_SZ)], ctypes.c_int),
+    "w8a8_mx4_quant": ([_P, _I64, _I64, _I64, _P, _SZ, _P], ctypes.c_int),
+    "w8a8_mx4_pack": ([_P, _P, _I64, _I64, _P, _SZ, _P], ctypes.c_int),
+    "w8a8_mx4_unpack": ([_P, _I64, _I64, _P, _P, _P], ctypes.c_int),
+    "w8a8_mx4_dequant": ([_P, _I64, _I64, _P, _P], ctypes.c_int),
+    "w8a8_mx4_scaled_mm_workspace_bytes": ([_I64, _I64, _I64, ctypes.POINTER(_SZ)], ctypes.c_int),
+    "w8a8_mx4_scaled_mm": ([_P, _P, _P, _P, _I64, _I64, _I64, ctypes.c_int, _P, _SZ, _P],
+                           ctypes.c_int),
+    "w8a8_mx4_scaled_mm_quant": ([_P, _P, _P, _P, _SZ, _I64, _I64, _I64, ctypes.c_int, _P, _SZ, _P],
+                                 ctypes.c_int),
+    "w8a8_mx4_linear_workspace_bytes": ([_I64, _I64, _I64, ctypes.POINTER(_SZ)], ctypes.c_int),
+    "w8a8_mx4_linear": ([_P, _I64, _P, _P, _P, _I64, _I64, _I64, ctypes.c_int, _P, _SZ, _P],
+                        ctypes.c_int),
+    "w8a8_mx4_linear_quant": ([_P, _I64, _P, _P, _P, _SZ, _I64, _I64, _I64, ctypes.c_int, _P, _SZ,
+                               _P], ctypes.c_int),
     "w8a8_set_path": ([ctypes.c_int], ctypes.c_int),
     "w8a8_gemm_kernel_name": ([_I64, _I64, _I64], ctypes.c_char_p),
     "w8a8_gelu_tanh": ([_P, _P, _I64, _P], ctypes.c_int),
