@@ -364,6 +364,61 @@ w8a8_status w8a8_mx4_linear_quant(const void *x, int64_t ldx, const void *w_imag
                                   void *y_image, size_t y_image_bytes, int64_t M, int64_t N, int64_t K,
                                   int act, void *workspace, size_t ws_bytes, w8a8_stream_t stream);
 
+/* ---- the norms around a block, with its gate and residual ---------------------
+ * No counterpart on the pages: what a transformer runs between two blocks of
+ * quantised layers, in one kernel that reads x and the residual stream once.
+ *   u = post(x)                                   (or x, without a post norm)
+ *   v = residual_scale * residual + gate[g] * u   (or x, without a residual)
+ *       rounded to the residual's type and stored as residual_out
+ *   h = pre(v) * (1 + scale[g]) + shift[g]
+ *   y = bf16(h); q, a_scale = the int8 codes and scales of y, as
+ *   w8a8_quant_act forms them; image = the 4-bit image of y, as w8a8_mx4_quant
+ *   forms it (bit for bit in both cases).  Any of the three may be asked for.
+ * Norms: rms(t) = t * rsqrt(mean(t^2) + eps) * weight + bias;
+ *   layer(t) the same of t - mean(t).  Weight and bias may be NULL (1 and 0).
+ * All sums and steps in fp32, rounded where stored.
+ * g is the row's group (image, sequence): group_index[m], or m /
+ * rows_per_group.  A row whose group_index is outside [0, groups) is padding:
+ * it is not computed and its outputs keep what they held.
+ * Limits: K % 8 == 0 (K % 16 == 0 with q or image), K <= 32768, strides in
+ * elements and multiples of 16 bytes, all pointers 16-byte aligned
+ * (group_index 4).  residual_out may be residual (with the same stride);
+ * otherwise outputs do not overlap inputs. */
+typedef enum { W8A8_NORM_NONE = 0, W8A8_NORM_RMS = 1, W8A8_NORM_LAYER = 2 } w8a8_norm_kind;
+typedef enum { W8A8_DTYPE_BF16 = 0, W8A8_DTYPE_FP32 = 1 } w8a8_dtype;
+
+typedef struct {
+  int kind;           /* w8a8_norm_kind */
+  float eps;          /* > 0 */
+  const void *weight; /* device, bf16 [K], or NULL */
+  const void *bias;   /* device, bf16 [K], or NULL */
+} w8a8_norm;
+
+typedef struct {
+  int64_t M, K;
+  const void *x; /* device, bf16 [M, K]: the block's output, or the stream itself */
+  int64_t ldx;
+  const void *residual; /* device [M, K], or NULL: no gate, no post norm, no residual_out */
+  void *residual_out;   /* device [M, K], the residual's type */
+  int64_t ldr, ldro;
+  int residual_dtype; /* w8a8_dtype */
+  float residual_scale;
+  w8a8_norm post, pre;
+  const void *gate, *scale, *shift; /* device, bf16 [groups, K], each may be NULL */
+  int64_t ld_gate, ld_scale, ld_shift; /* row strides; 0: one row for every group */
+  int64_t groups;             /* rows of gate, scale and shift */
+  int64_t rows_per_group;     /* without group_index: groups * rows_per_group >= M */
+  const int32_t *group_index; /* device, int32 [M], or NULL */
+  void *y; /* device, bf16 [M, K], or NULL */
+  int64_t ldy;
+  int8_t *q;      /* device, int8 [M, K] dense, or NULL */
+  float *a_scale; /* device, fp32 [M], with q */
+  void *image;    /* device, 4-bit image of [M, K], or NULL */
+  size_t image_bytes;
+} w8a8_block_norm_args;
+
+w8a8_status w8a8_block_norm(const w8a8_block_norm_args *args, w8a8_stream_t stream);
+
 /* ---- path selection (tests and benchmarks) ---------------------------------
  * 0 = automatic (default); 1 = always the persistent large-M GEMM (automatic
  * tile width); 2 = the small-M weight-streaming kernel (M <= 16 only, else

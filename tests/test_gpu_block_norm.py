@@ -1,0 +1,189 @@
+"""GPU tests of the fused norms around a block against the plain form in 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+import w8a8_int8_dynamic_b200 as w8
+from gpu_util import require_gpu
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24                                   # a rounding in fp32, relative
+HALF = torch.finfo(torch.bfloat16).eps / 2
+#: roundings on the longest way through the kernel's sum over a row: 64 elements of a lane one after
+#: another, 5 shuffles, 16 warps, the factor 1/K and its own rounding
+DEPTH = 64 + 5 + 16 + 2
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    require_gpu()
+    yield
+    assert w8.poll_status() == 0
+
+
+def f64(t):
+    return None if t is None else t.double().cpu().numpy()
+
+
+def norm64(t, n):
+    """(norm of t, bound on the fp32 kernel's error): the sums' roundings, those of the differences and
+    products, and two ulps (2^-22) of the reciprocal root."""
+    layer = n.kind == "layer"
+    mean = t.mean(1, keepdims=True) if layer else np.zeros((len(t), 1))
+    d = t - mean
+    e_d = U * (DEPTH * np.abs(t).mean(1, keepdims=True) + np.abs(mean) + np.abs(d)) if layer else np.zeros_like(t)
+    var = (d * d).mean(1, keepdims=True) + n.eps
+    rel = (DEPTH + 2) * U / 2 + (np.abs(d) * e_d).mean(1, keepdims=True) / var + 2.0 ** -22
+    z = d / np.sqrt(var)
+    e_z = e_d / np.sqrt(var) + np.abs(z) * (rel + U)
+    w = 1.0 if n.weight is None else f64(n.weight)
+    b = 0.0 if n.bias is None else f64(n.bias)
+    return z * w + b, np.abs(w) * e_z + 2 * U * (np.abs(z * w) + np.abs(b))
+
+
+def rows(v, index, M):
+    return 0.0 if v is None else f64(v).reshape(-1, v.shape[-1])[index]
+
+
+def check(out, x, residual, kw, index):
+    """The stream against the formula, then the output against the formula of the stream as it was stored."""
+    t, err = f64(x), 0.0
+    stream = t
+    if residual is not None:
+        if kw.get("post"):
+            t, err = norm64(t, kw["post"])
+        gate = 1.0 if kw.get("gate") is None else rows(kw["gate"], index, len(t))
+        r = kw.get("residual_scale", 1.0) * f64(residual)
+        want = r + gate * t
+        err = np.abs(gate) * err + 2 * U * (np.abs(r) + np.abs(gate * t))
+        got = f64(out.residual)
+        half = HALF if residual.dtype == torch.bfloat16 else U
+        assert (np.abs(got - want) <= err + half * (np.abs(want) + err)).all()
+        stream = got
+    if not kw.get("pre"):
+        return
+    h, err = norm64(stream, kw["pre"])
+    s, sh = 1 + rows(kw.get("scale"), index, len(h)), rows(kw.get("shift"), index, len(h))
+    want = h * s + sh
+    err = np.abs(s) * err + 2 * U * (np.abs(h * s) + np.abs(sh))
+    assert (np.abs(f64(out.y) - want) <= err + HALF * (np.abs(want) + err)).all()
+
+
+def tensors(seed, M, K, groups=0, dtype=torch.bfloat16, mean=0.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def n(*shape, std=1.0, m=0.0):
+        return (torch.randn(*shape, device="cuda", generator=g) * std + m).bfloat16()
+
+    x, r = n(M, K, m=mean), n(M, K, std=2.0).to(dtype)
+    x[:, :: max(1, K // 7)] *= 10
+    if M > 1:
+        x[M // 2] = 0  # a row of zeros
+    mod = n(groups, 3 * K, std=0.5).split(K, 1) if groups else (None,) * 3
+    return x, r, (n(K, std=0.2, m=1.0), n(K, std=0.2)), (n(K, std=0.2, m=1.0), n(K, std=0.2)), mod
+
+
+SHAPES = [(1, 8), (1, 5120), (3, 24), (5, 264), (7, 1000), (130, 2048), (33, 4104), (4, 12288), (2, 16392), (2, 32768)]
+
+
+@pytest.mark.parametrize("M,K", SHAPES)
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_norm_before(M, K, kind):
+    x, _, (w, b), _, (_, scale, shift) = tensors(M + K, M, K, groups=1, mean=3.0)
+    for kw in ({}, {"scale": scale, "shift": shift}, {"shift": shift[0]}):
+        kw["pre"] = w8.Norm(kind, w, b if kw else None, 1e-5)
+        check(w8.block_norm(x, **kw), x, None, kw, np.zeros(M, int))
+
+
+@pytest.mark.parametrize("M,K", SHAPES)
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_norms_around_the_residual(M, K, kind, dtype):
+    groups = min(M, 3)
+    x, r, (pw, pb), (w, b), (gate, scale, shift) = tensors(M * 3 + K, M, K, groups, dtype)
+    per = -(-M // groups)
+    kw = dict(post=w8.Norm(kind, pw, pb, 1e-6), gate=gate, residual_scale=0.7, pre=w8.Norm(kind, w, b, 1e-6),
+              scale=scale, shift=shift, rows_per_group=per)
+    check(w8.block_norm(x, r, **kw), x, r, kw, np.arange(M) // per)
+    # each part alone
+    for kw in ({}, {"gate": gate, "rows_per_group": per}, {"post": w8.Norm(kind, pw)}, {"pre": w8.Norm(kind)}):
+        out = w8.block_norm(x, r, **kw)
+        check(out, x, r, kw, np.arange(M) // per)
+        assert (out.y is None) == ("pre" not in kw)
+
+
+@pytest.mark.parametrize("M,K", [(1, 16), (1, 5120), (5, 272), (129, 1040), (300, 2048), (3, 12288), (2, 32768)])
+@pytest.mark.parametrize("codes", ["int8", "mx4"])
+def test_codes_are_those_of_the_output(M, K, codes):
+    x, r, (pw, _), (w, b), (gate, scale, shift) = tensors(M + 5 * K, M, K, 1)
+    kw = dict(post=w8.Norm("rms", pw), gate=gate, pre=w8.Norm("layer", w, b), scale=scale, shift=shift, codes=codes)
+    out = w8.block_norm(x, r, y=True, **kw)
+    assert torch.equal(out.y, w8.block_norm(x, r, **{**kw, "codes": None}).y)
+    alone = w8.block_norm(x, r, **kw)
+    assert alone.y is None
+    if codes == "int8":
+        q, s = w8.quant_act(out.y)
+        for o in (out, alone):
+            assert torch.equal(o.q, q) and torch.equal(o.a_scale, s)
+    else:
+        want = w8.mx4_quant(out.y)
+        for o in (out, alone):
+            # to the end of the last tile: its padding is zeros
+            padded = -(-K // 256) * 256
+            for g, v in zip(w8.MX4Tensor(o.mx4.image, (M,), padded).unpack(),
+                            w8.MX4Tensor(want.image, (M,), padded).unpack()):
+                assert torch.equal(g, v)
+
+
+def test_rows_of_zeros_infinities_and_nan():
+    x, r, _, (w, b), _ = tensors(9, 6, 512)
+    x[1], x[2, 5], x[3, 6] = 0, float("inf"), float("nan")
+    clean = [0, 1, 4, 5]
+    for kind in ("rms", "layer"):
+        n = w8.Norm(kind, w, b)
+        out = w8.block_norm(x, pre=n, y=True, codes="mx4")
+        ok = w8.block_norm(x[clean], pre=n)
+        assert torch.equal(out.y[clean], ok.y)
+        assert out.y[3].isnan().all() and out.y[2].isnan().any()
+        assert torch.isfinite(out.y[1]).all()
+        assert out.mx4.dequant()[3].isnan().all()
+
+
+def test_group_index_and_padding_rows():
+    M, K, groups = 37, 1040, 4
+    x, r, (pw, _), (w, _), (gate, scale, shift) = tensors(11, M, K, groups)
+    index = torch.randint(0, groups, (M,), dtype=torch.int32, device="cuda")
+    skip = [0, 17, 36]
+    index[skip[0]], index[skip[1]], index[skip[2]] = -1, groups, 2 ** 31 - 1
+    keep = [m for m in range(M) if m not in skip]
+    kw = dict(post=w8.Norm("rms", pw), gate=gate, pre=w8.Norm("layer", w), scale=scale, shift=shift)
+    stream = r.clone()
+    out = w8.block_norm(x, stream, residual_out=stream, group_index=index, codes="mx4", y=True, **kw)
+    assert out.residual.data_ptr() == stream.data_ptr()
+    assert torch.equal(stream[skip], r[skip])
+    for g in range(groups):
+        at = [m for m in keep if index[m] == g]
+        if not at:
+            continue
+        one = w8.block_norm(x[at], r[at], **{**kw, "gate": gate[g], "scale": scale[g], "shift": shift[g]})
+        assert torch.equal(stream[at], one.residual) and torch.equal(out.y[at], one.y)
+    # an image given rows to leave alone: the other rows' codes are those of y
+    c, s = out.mx4.unpack()
+    cw, sw = w8.mx4_quant(out.y).unpack()
+    assert torch.equal(c[keep], cw[keep]) and torch.equal(s[keep], sw[keep])
+
+
+def test_strides_and_leading_sizes():
+    x, r, _, (w, _), _ = tensors(13, 24, 528)
+    n = w8.Norm("rms", w)
+    want = w8.block_norm(x, r, pre=n)
+    wide_x, wide_r = torch.zeros(24, 1000, dtype=torch.bfloat16, device="cuda"), torch.zeros(24, 800, device="cuda")
+    wide_x[:, 8:536], wide_r[:, 4:532] = x, r.float()
+    got = w8.block_norm(wide_x[:, 8:536], wide_r[:, 4:532], residual_out=wide_r[:, 4:532], pre=n)
+    assert torch.equal(wide_r[:, 4:532].bfloat16(), want.residual)
+    assert not wide_r[:, :4].any() and not wide_r[:, 532:].any()
+    shaped = w8.block_norm(x.view(2, 3, 4, 528), r.view(2, 3, 4, 528), pre=n, codes="int8", y=True)
+    assert shaped.residual.shape == shaped.y.shape == shaped.q.shape == (2, 3, 4, 528)
+    assert torch.equal(shaped.y.view(24, 528), want.y) and got.y.shape == (24, 528)
+    assert w8.block_norm(x[:0], r[:0], pre=n, codes="mx4").residual.shape == (0, 528)

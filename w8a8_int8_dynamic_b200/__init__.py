@@ -17,3 +17,4 @@ from .mx4 import (  # noqa: F401
     MX4Linear, MX4Tensor, mx4_bytes, mx4_dequant, mx4_linear, mx4_linear_quant,
     mx4_linear_workspace_bytes, mx4_pack, mx4_quant, mx4_scaled_mm, mx4_scaled_mm_quant,
     mx4_scaled_mm_workspace_bytes, mx4_unpack)
+from .norms import BlockNormOutput, Norm, block_norm  # noqa: F401

@@ -85,6 +85,7 @@ _SIGNATURES = {
                         ctypes.c_int),
     "w8a8_mx4_linear_quant": ([_P, _I64, _P, _P, _P, _SZ, _I64, _I64, _I64, ctypes.c_int, _P, _SZ,
                                _P], ctypes.c_int),
+    "w8a8_block_norm": ([_P, _P], ctypes.c_int),
     "w8a8_set_path": ([ctypes.c_int], ctypes.c_int),
     "w8a8_gemm_kernel_name": ([_I64, _I64, _I64], ctypes.c_char_p),
     "w8a8_gelu_tanh": ([_P, _P, _I64, _P], ctypes.c_int),
@@ -449,6 +450,15 @@ class W8A8Linear:
             self._ws = torch.empty((need,), dtype=torch.uint8, device=x.device)
         return linear(x, self.packed, self.w_scale, self.bias, self.N, workspace=self._ws,
                       act=self.act)
+
+    def apply_codes(self, q: torch.Tensor, a_scale: torch.Tensor,
+                    out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """The layer on activations that are codes already (int8 [..., K] and their fp32
+        scales, as ``quant_act`` or ``block_norm`` forms them): y bf16 [..., N]."""
+        lead = q.shape[:-1]
+        y = scaled_mm(q.reshape(-1, self.K), a_scale, self.packed, self.w_scale, self.bias, self.N,
+                      out=out, stream=stream, act=self.act)
+        return y.view(*lead, self.N)
 
     def split(self, y: torch.Tensor):
         return torch.split(y, list(self.splits), dim=-1)
