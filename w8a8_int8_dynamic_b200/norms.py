@@ -7,9 +7,10 @@ from typing import NamedTuple, Optional
 import torch
 
 from .binding import _P, _SZ, _check, _need_cuda, lib
-from .mx4 import MX4Tensor, _device, _on, _rows_of, mx4_bytes
+from .mx4 import MX4Tensor, _call, _device, _rows_of, mx4_bytes
 
 _KINDS = {"rms": 1, "layer": 2}
+_RESIDUAL = {torch.bfloat16: 0, torch.float32: 1}
 _I64 = ctypes.c_int64
 
 
@@ -44,22 +45,17 @@ class _Args(ctypes.Structure):
                 ("image_bytes", _SZ)]
 
 
-def _norm(norm: Optional[Norm], K: int) -> _NormStruct:
-    if norm is None:
-        return _NormStruct(0, 0.0, None, None)
-    if norm.kind not in _KINDS:
+def _set_norm(to: _NormStruct, norm: Norm, K: int):
+    kind = _KINDS.get(norm.kind)
+    if kind is None:
         raise ValueError(f"norm kind must be one of {sorted(_KINDS)}, got {norm.kind!r}")
+    to.kind, to.eps = kind, norm.eps
     for name, t in (("weight", norm.weight), ("bias", norm.bias)):
         if t is not None:
             _need_cuda(t, f"norm {name}", torch.bfloat16)
             if t.numel() != K or not t.is_contiguous():
                 raise ValueError(f"norm {name} must be contiguous and hold {K} values")
-    return _NormStruct(_KINDS[norm.kind], norm.eps, None if norm.weight is None else norm.weight.data_ptr(),
-                       None if norm.bias is None else norm.bias.data_ptr())
-
-
-def _address(t: Optional[torch.Tensor]) -> Optional[int]:
-    return None if t is None else t.data_ptr()
+            setattr(to, name, t.data_ptr())
 
 
 def block_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, *, post: Optional[Norm] = None,
@@ -93,44 +89,54 @@ def block_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, *, post
         raise ValueError("post, gate and residual_out need a residual")
     if residual is None and pre is None:
         raise ValueError("nothing to compute: give residual, pre or both")
-    dev = _device(x, residual, gate, scale, shift, group_index, residual_out,
-                  *(t for n in (post, pre) if n is not None for t in (n.weight, n.bias)))
-    a = _Args(K=K, post=_norm(post, K), pre=_norm(pre, K), residual_scale=residual_scale)
-    with _on(dev, stream) as s:
-        x2, a.ldx = _rows_of(x)
-        M = a.M = x2.shape[0]
-        a.x = x2.data_ptr()
+    index = _device(x, residual, gate, scale, shift, group_index, residual_out,
+                    *(t for n in (post, pre) if n is not None for t in (n.weight, n.bias)))
+    if residual is not None:
+        _need_cuda(residual, "residual")
+        if residual.dtype not in _RESIDUAL:
+            raise ValueError(f"residual must be bf16 or fp32, got {residual.dtype}")
+        if residual.shape != x.shape:
+            raise ValueError(f"residual must have x's shape {list(x.shape)}, got {list(residual.shape)}")
+        if residual_out is not None and (residual_out.dtype != residual.dtype or residual_out.shape != x.shape):
+            raise ValueError("residual_out must have the residual's type and shape")
+    want_y = pre is not None and (codes is None if y is None else y)
+    if pre is not None and codes is None and not want_y:
+        raise ValueError("y=False leaves no output for the norm: ask for codes")
 
+    def f(s):
+        x2, M, ldx = _rows_of(x)
+        a = _Args(M=M, K=K, x=x2.data_ptr(), ldx=ldx, residual_scale=residual_scale)
+        if post is not None:
+            _set_norm(a.post, post, K)
+        if pre is not None:
+            _set_norm(a.pre, pre, K)
         new = None
+        held = [x2]  # what a copy was made of, until the launch
         if residual is not None:
-            _need_cuda(residual, "residual")
-            if residual.dtype not in (torch.bfloat16, torch.float32):
-                raise ValueError(f"residual must be bf16 or fp32, got {residual.dtype}")
-            if residual.shape != x.shape:
-                raise ValueError(f"residual must have x's shape {list(x.shape)}, got {list(residual.shape)}")
-            new = torch.empty(x.shape, dtype=residual.dtype, device=dev) if residual_out is None else residual_out
-            if new.dtype != residual.dtype or new.shape != x.shape:
-                raise ValueError("residual_out must have the residual's type and shape")
-            r2, a.ldr = _rows_of(residual)
-            # written in place: a view, never a copy
-            n2 = new.view(-1, K) if new.is_contiguous() else new
-            if n2.dim() != 2 or (M and n2.stride(1) != 1):
-                raise ValueError("residual_out must be contiguous, or [rows, K] with unit stride along K")
-            a.ldro = n2.stride(0) if M > 1 else K
-            a.residual, a.residual_out = r2.data_ptr(), n2.data_ptr()
-            a.residual_dtype = 1 if residual.dtype == torch.float32 else 0
+            r2, _, a.ldr = _rows_of(residual)
+            held.append(r2)
+            if residual_out is None:
+                new, a.ldro = torch.empty(x.shape, dtype=residual.dtype, device=index), K
+            else:  # written in place: a view, never a copy
+                new = residual_out
+                n2 = new.view(-1, K) if new.is_contiguous() else new
+                if n2.dim() != 2 or (M and n2.stride(1) != 1):
+                    raise ValueError("residual_out must be contiguous, or [rows, K] with unit stride along K")
+                a.ldro = n2.stride(0) if M > 1 else K
+            a.residual, a.residual_out = r2.data_ptr(), new.data_ptr()
+            a.residual_dtype = _RESIDUAL[residual.dtype]
 
-        held, groups = [], None
+        groups = 0
         for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
             if t is None:
                 continue
             _need_cuda(t, name, torch.bfloat16)
-            t = t.view(1, -1) if t.dim() == 1 else t
-            if t.dim() != 2 or t.shape[1] != K or (groups is not None and t.shape[0] != groups):
+            if t.dim() == 1:
+                t = t.view(1, -1)
+            if t.dim() != 2 or t.shape[1] != K or (groups and t.shape[0] != groups):
                 raise ValueError(f"{name} must be [groups, {K}], with as many groups as the others, "
                                  f"got {list(t.shape)}")
-            groups = t.shape[0]
-            t, ld = _rows_of(t)
+            t, groups, ld = _rows_of(t)
             held.append(t)
             setattr(a, name, t.data_ptr())
             setattr(a, "ld_" + name, ld)
@@ -139,24 +145,25 @@ def block_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, *, post
             if group_index.numel() != M or not group_index.is_contiguous():
                 raise ValueError(f"group_index must be contiguous and hold {M} values")
             a.group_index = group_index.data_ptr()
-            groups = 1 if groups is None else groups
-        a.groups = groups or 0
-        a.rows_per_group = max(M, 1) if rows_per_group is None else rows_per_group
+            groups = groups or 1
+        if groups:
+            a.groups = groups
+            a.rows_per_group = (M or 1) if rows_per_group is None else rows_per_group
 
-        want_y = pre is not None and (codes is None if y is None else y)
-        if pre is not None and codes is None and not want_y:
-            raise ValueError("y=False leaves no output for the norm: ask for codes")
-        out = torch.empty(x.shape, dtype=torch.bfloat16, device=dev) if want_y else None
-        a.y, a.ldy = _address(out), K
-        q = a_scale = image = None
+        out = q = a_scale = image = None
+        if want_y:
+            out = torch.empty(x.shape, dtype=torch.bfloat16, device=index)
+            a.y, a.ldy = out.data_ptr(), K
         if codes == "int8":
-            q = torch.empty(x.shape, dtype=torch.int8, device=dev)
-            a_scale = torch.empty((M,), dtype=torch.float32, device=dev)
-            a.q, a.a_scale = _address(q), _address(a_scale)
+            q = torch.empty(x.shape, dtype=torch.int8, device=index)
+            a_scale = torch.empty((M,), dtype=torch.float32, device=index)
+            a.q, a.a_scale = q.data_ptr(), a_scale.data_ptr()
         elif codes == "mx4":
             a.image_bytes = mx4_bytes(M, K) if M else 0
-            image = torch.empty((a.image_bytes,), dtype=torch.uint8, device=dev)
+            image = torch.empty((a.image_bytes,), dtype=torch.uint8, device=index)
             a.image = image.data_ptr()
         if M:
-            _check(lib().w8a8_block_norm(ctypes.byref(a), ctypes.c_void_p(s.cuda_stream)), "w8a8_block_norm")
-    return BlockNormOutput(new, out, q, a_scale, None if image is None else MX4Tensor(image, x.shape[:-1], K))
+            _check(lib().w8a8_block_norm(ctypes.byref(a), s), "w8a8_block_norm")
+        return BlockNormOutput(new, out, q, a_scale,
+                               None if image is None else MX4Tensor(image, x.shape[:-1], K))
+    return _call(index, stream, f)
