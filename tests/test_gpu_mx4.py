@@ -157,3 +157,24 @@ def test_product_with_codes_of_its_output(M, N, K, act):
     padded = -(-N // 256) * 256
     c, s = w8.MX4Tensor(t.image, (M,), padded).unpack()
     assert not c[:, N // 2:].any() and not (s[:, -(-N // 32):] == 255).any()
+
+
+@pytest.mark.parametrize("path", [w8.PATH_LARGE, w8.PATH_SMALL])
+@pytest.mark.parametrize("M,N,K", [(1, 1000, 5120), (4, 520, 13824), (16, 4096, 1040), (16, 136, 8208),
+                                   (17, 4096, 528), (64, 2056, 4112), (128, 1032, 2064), (100, 8, 16384)])
+def test_product_of_few_rows_on_either_path(M, N, K, path):
+    """Slabs of one and of many contributors, short and long K: both kernels, twice, y and its codes."""
+    x, w, b = operands(M + N + K, M, N, K)
+    a = w8.mx4_quant(x)
+    w8.set_path(path)
+    try:
+        y = w8.mx4_linear(x, w, b)
+        check_product(y, a, w, b, w8.ACT_NONE)
+        for _ in range(5):  # the same bits, whoever finishes a slab
+            assert torch.equal(w8.mx4_linear(x, w, b), y)
+            assert torch.equal(w8.mx4_scaled_mm(a, w, b), y)
+        if N % 16 == 0:
+            t = w8.mx4_linear_quant(x, w, b)
+            assert all(torch.equal(g, v) for g, v in zip(t.unpack(), w8.mx4_quant(y).unpack()))
+    finally:
+        w8.set_path(w8.PATH_AUTO)

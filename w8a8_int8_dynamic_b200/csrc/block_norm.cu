@@ -18,8 +18,8 @@
 // (2 + r) bytes read and (r + 2 | 1 | 17/32) written an element, r the bytes of
 // the residual's type.
 //
-// The kernel releases its programmatic dependents once the kernel before it
-// is complete.
+// A programmatic dependent that releases the next kernel at its start and
+// touches memory only after its own wait.
 #include <algorithm>
 
 #include "mx4_common.cuh"
@@ -131,8 +131,8 @@ __device__ __forceinline__ void normalise(float (&t)[CPL][8], int kind, float ep
 template <int CPL>
 __global__ void __launch_bounds__(512) block_norm_kernel(const NormArgs a) {
   __shared__ float lines[5][kMaxWarps];
-  griddep_wait();
   griddep_launch_dependents();
+  griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int W = a.W, rl = warp / W, w = warp - rl * W;
   const int64_t row = (int64_t)blockIdx.x * a.R + rl;

@@ -141,9 +141,7 @@ w8a8_status launch_decode(const int8_t *q, const float *a_scale, const void *pac
 w8a8_status launch_quant(const void *x, int64_t M, int64_t K, int64_t ldx, int8_t *q,
                          float *a_scale, cudaStream_t stream, bool ahead_of_gemm,
                          uint32_t *zero_rows = nullptr);
-// Microscaled 4-bit quantisation (mx4_quant.cu): bf16 [rows, K] -> image.  The
-// kernel releases its programmatic dependents once the kernel before it is
-// complete.
+// Microscaled 4-bit quantisation (mx4_quant.cu): bf16 [rows, K] -> image.
 w8a8_status launch_mx4_quant(const void *x, int64_t rows, int64_t K, int64_t ldx, void *image,
                              cudaStream_t stream);
 

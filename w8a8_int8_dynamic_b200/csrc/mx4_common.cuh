@@ -199,6 +199,13 @@ struct Mx4Args {
   int *status;
 };
 
+// Few rows (mx4_stream.cu), M <= kStreamRows.  x: bf16 rows that the kernel
+// quantises itself (M <= kStreamQuantRows), or null: p.a is their image.
+constexpr int64_t kStreamRows = 128, kStreamQuantRows = 16;
+int64_t mx4_stream_workspace_bytes(int64_t M, int64_t N, int64_t K);
+w8a8_status launch_mx4_stream(const Mx4Args &p, const void *x, int64_t ldx, int64_t K, void *workspace,
+                              cudaStream_t stream);
+
 // The bias, activation and rounding of 8 consecutive outputs of a row.
 __device__ __forceinline__ uint4 mx4_finish8(const uint32_t *acc, const uint16_t *bias, int act) {
   float t[8];

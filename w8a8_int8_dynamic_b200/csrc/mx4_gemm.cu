@@ -135,17 +135,15 @@ __global__ void __maxnreg__(kGemmRegs)
     const uint32_t pre = total < kMxStages ? (uint32_t)total : (uint32_t)kMxStages;
     int64_t issued = 0;
     Cursor cur = enter(0);
-    const Cursor first = cur;
-    for (uint32_t s = 0; s < pre; ++s) {  // weights do not depend on the preceding kernel
+    // before the wait for the preceding kernel, the first weights are only
+    // asked into L2 (see mx4_stream.cu)
+    if (total > 0) bulk_prefetch_l2(cur.w, (uint32_t)(min(kt, kMxStages) * kMxTileBytes));
+    griddep_wait();
+    for (uint32_t s = 0; s < pre; ++s) {
       mbar_arrive_expect_tx(&full[s], kMxStageBytes);
       weights(cur, s);
+      acts(cur, s);
       next(cur);
-    }
-    griddep_wait();
-    Cursor c = first;
-    for (uint32_t s = 0; s < pre; ++s) {
-      acts(c, s);
-      next(c);
     }
     uint32_t s = 0, ph = 1;
     for (issued = pre; issued < total; ++issued) {
@@ -290,7 +288,7 @@ __global__ void __maxnreg__(kGemmRegs)
 
 FuncAttrOnce g_mx_smem_attr;
 
-w8a8_status launch_mx4_1sm(const CUtensorMap &ty, Mx4Args a, cudaStream_t stream, bool pdl) {
+w8a8_status launch_mx4_1sm(const CUtensorMap &ty, Mx4Args a, cudaStream_t stream) {
   if (g_mx_smem_attr.ensure([] {
         return cudaFuncSetAttribute(mx4_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     MxSmem::kAlloc);
@@ -309,18 +307,23 @@ w8a8_status launch_mx4_1sm(const CUtensorMap &ty, Mx4Args a, cudaStream_t stream
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = pdl ? attr : nullptr;
-  cfg.numAttrs = pdl ? 1 : 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, mx4_gemm_kernel, ty, a);
   if (e == cudaSuccess) count_launch();
   return from_cuda(e);
 }
 
+// Up to 128 rows the weight stream sets the time (mx4_stream.cu).
+bool use_stream(int64_t M) {
+  const int p = forced_path();
+  return M <= kStreamRows && (p == 0 || p == 2);
+}
+
+// x (with ldx; a layer of few rows): quantised by the product itself, in place of a_image.
 w8a8_status launch_mx4(const void *a_image, const void *w_image, const void *bias, void *y,
                        void *y_image, int64_t M, int64_t N, int64_t K, int act, void *workspace,
-                       size_t ws_bytes, cudaStream_t stream, bool pdl) {
-  (void)workspace;
-  (void)ws_bytes;
+                       const void *x, int64_t ldx, cudaStream_t stream) {
   Mx4Args a{};
   a.a = static_cast<const uint8_t *>(a_image);
   a.w = static_cast<const uint8_t *>(w_image);
@@ -334,9 +337,11 @@ w8a8_status launch_mx4(const void *a_image, const void *w_image, const void *bia
   a.act = act;
   a.status = status_word();
   if (!a.status) return W8A8_ERR_CUDA;
+  if (forced_path() == 2 && M > kStreamRows) return W8A8_ERR_INVALID_ARG;
+  if (use_stream(M)) return launch_mx4_stream(a, x, ldx, K, workspace, stream);
   CUtensorMap ty = {};
   if (y && !make_tmap_out_bf16(&ty, y, (uint64_t)M, (uint64_t)N)) return W8A8_ERR_CUDA;
-  return launch_mx4_1sm(ty, a, stream, pdl);
+  return launch_mx4_1sm(ty, a, stream);
 }
 
 // The checks that every product shares.  `image`: the output is an image (the
@@ -354,8 +359,7 @@ w8a8_status check_product(const void *w_image, const void *bias, const void *y, 
 }
 
 int64_t product_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  (void)M, (void)N, (void)K;
-  return 0;
+  return M <= kStreamRows ? mx4_stream_workspace_bytes(M, N, K) : 0;
 }
 
 w8a8_status product(const void *a_image, const void *w_image, const void *bias, void *y, void *y_image,
@@ -368,7 +372,7 @@ w8a8_status product(const void *a_image, const void *w_image, const void *bias, 
       (workspace ? ws_bytes : 0) < (size_t)product_workspace_bytes(M, N, K))
     return W8A8_ERR_BUFFER_TOO_SMALL;
   return launch_mx4(a_image, w_image, bias, image ? nullptr : y, image ? y_image : nullptr, M, N, K,
-                    act, workspace, ws_bytes, reinterpret_cast<cudaStream_t>(stream), false);
+                    act, workspace, nullptr, 0, reinterpret_cast<cudaStream_t>(stream));
 }
 
 // A layer's workspace: the image of x, then the product's.
@@ -388,9 +392,11 @@ w8a8_status layer(const void *x, int64_t ldx, const void *w_image, const void *b
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   const int64_t head = round_up(mx4_image_bytes(M, K), 256);
-  if (const w8a8_status r = launch_mx4_quant(x, M, K, ldx, ws, s)) return r;
+  const bool fused = use_stream(M) && M <= kStreamQuantRows;
+  if (!fused)
+    if (const w8a8_status r = launch_mx4_quant(x, M, K, ldx, ws, s)) return r;
   return launch_mx4(ws, w_image, bias, image ? nullptr : y, image ? y_image : nullptr, M, N, K, act,
-                    ws + head, ws_bytes - (size_t)head, s, true);
+                    ws + head, fused ? x : nullptr, ldx, s);
 }
 
 w8a8_status size_query(int64_t M, int64_t N, int64_t K, size_t *bytes, int64_t (*f)(int64_t, int64_t, int64_t)) {

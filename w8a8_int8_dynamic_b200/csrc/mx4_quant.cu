@@ -8,6 +8,10 @@
 // of exact values; the warp's 32 code words are one full 128-byte line of the
 // image (permuted by the swizzle).  All of a warp's rows are loaded before
 // the first is used.  HBM-bound: 2 bytes read and 17/32 written an element.
+//
+// All kernels of the 4-bit layers are programmatic dependents that release the
+// next kernel at their start and read and write global memory only after their
+// own wait, so any of them may follow any kernel.
 #include <algorithm>
 
 #include "mx4_common.cuh"
@@ -22,15 +26,12 @@ __device__ __forceinline__ uint8_t *tile_of(uint8_t *image, int64_t slab, int kt
   return image + ((size_t)slab * kt + ktile) * kMxTileBytes;
 }
 
-// grid: (K tiles, row slabs).  PDL: waits for the preceding kernel before it
-// reads x or writes the image, and releases the next one only then (a product
-// launched behind this kernel reads its weights before it waits: they must
-// not be the output of a kernel that this one still waits for).
+// grid: (K tiles, row slabs).
 __global__ void __launch_bounds__(kQuantThreads)
     mx4_quant_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t rows, int K, int kt,
                      uint8_t *__restrict__ image) {
-  griddep_wait();
   griddep_launch_dependents();
+  griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t slab = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
   const int64_t row0 = slab * kMxTileRows;
@@ -118,8 +119,8 @@ __global__ void __launch_bounds__(256)
 __global__ void __launch_bounds__(kQuantThreads)
     mx4_dequant_kernel(const uint8_t *__restrict__ image, int64_t rows, int K, int kt,
                        uint16_t *__restrict__ x) {
-  griddep_wait();
   griddep_launch_dependents();
+  griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t slab = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
   const int64_t row0 = slab * kMxTileRows;
