@@ -178,3 +178,31 @@ def test_product_of_few_rows_on_either_path(M, N, K, path):
             assert all(torch.equal(g, v) for g, v in zip(t.unpack(), w8.mx4_quant(y).unpack()))
     finally:
         w8.set_path(w8.PATH_AUTO)
+
+
+@pytest.mark.parametrize("path", [w8.PATH_LARGE, w8.PATH_LARGE_PAIR])
+@pytest.mark.parametrize("M,N,K,act", [(1, 8, 16, 0), (128, 256, 256, 0), (129, 264, 272, 1), (256, 256, 4096, 0),
+                                       (300, 640, 1808, 1), (384, 1168, 528, 0), (1000, 1040, 784, 1),
+                                       (2600, 2064, 1040, 0), (700, 5136, 272, 0), (300, 512, 12304, 0)])
+def test_product_of_many_rows_on_either_path(M, N, K, act, path):
+    """Ragged tiles, several tiles a CTA, K from one step to more than the ring: both kernels, y and its codes."""
+    x, w, b = operands(M + N + K, M, N, K)
+    a = w8.mx4_quant(x)
+    w8.set_path(path)
+    try:
+        y = w8.mx4_linear(x, w, b, act=act)
+        check_product(y, a, w, b, act)
+        assert torch.equal(w8.mx4_scaled_mm(a, w, b, act=act), y)
+        if N % 16 == 0:
+            image = torch.full((w8.mx4_bytes(M, N),), 0xFF, dtype=torch.uint8, device="cuda")
+            t = w8.mx4_scaled_mm_quant(a, w, b, image=image, act=act)
+            padded = -(-N // 256) * 256
+            want = w8.mx4_quant(y)
+            for g, v in zip(w8.MX4Tensor(t.image, (M,), padded).unpack(),
+                            w8.MX4Tensor(want.image, (M,), padded).unpack()):
+                assert torch.equal(g, v)
+            if M % 128:  # rows behind the last one are left as they were
+                c, s = w8.MX4Tensor(t.image, (-(-M // 128) * 128,), padded).unpack()
+                assert (c[M:] == 255).all() and (s[M:] == 255).all()
+    finally:
+        w8.set_path(w8.PATH_AUTO)

@@ -206,6 +206,9 @@ int64_t mx4_stream_workspace_bytes(int64_t M, int64_t N, int64_t K);
 w8a8_status launch_mx4_stream(const Mx4Args &p, const void *x, int64_t ldx, int64_t K, void *workspace,
                               cudaStream_t stream);
 
+// Many rows (mx4_pair.cu): 256 x 256 tiles on CTA pairs.
+w8a8_status launch_mx4_pair(Mx4Args a, cudaStream_t stream);
+
 // The bias, activation and rounding of 8 consecutive outputs of a row.
 __device__ __forceinline__ uint4 mx4_finish8(const uint32_t *acc, const uint16_t *bias, int act) {
   float t[8];

@@ -320,6 +320,14 @@ bool use_stream(int64_t M) {
   return M <= kStreamRows && (p == 0 || p == 2);
 }
 
+bool use_pair(const Mx4Args &a) {
+  const int p = forced_path();
+  // (the pair kernel's box coordinates are 32-bit rows of 128 bytes)
+  const int64_t most = (std::max(mx4_slabs(a.M), mx4_slabs(a.N)) + 2) * a.kt * (kMxTileBytes / 128);
+  if (most > 0x7FFFFFFF || (p != 0 && p != 5 && p != 7)) return false;
+  return p != 0 || ((int64_t)a.M * a.N >= (int64_t)1024 * 4096);
+}
+
 // x (with ldx; a layer of few rows): quantised by the product itself, in place of a_image.
 w8a8_status launch_mx4(const void *a_image, const void *w_image, const void *bias, void *y,
                        void *y_image, int64_t M, int64_t N, int64_t K, int act, void *workspace,
@@ -339,6 +347,7 @@ w8a8_status launch_mx4(const void *a_image, const void *w_image, const void *bia
   if (!a.status) return W8A8_ERR_CUDA;
   if (forced_path() == 2 && M > kStreamRows) return W8A8_ERR_INVALID_ARG;
   if (use_stream(M)) return launch_mx4_stream(a, x, ldx, K, workspace, stream);
+  if (use_pair(a)) return launch_mx4_pair(a, stream);
   CUtensorMap ty = {};
   if (y && !make_tmap_out_bf16(&ty, y, (uint64_t)M, (uint64_t)N)) return W8A8_ERR_CUDA;
   return launch_mx4_1sm(ty, a, stream);
