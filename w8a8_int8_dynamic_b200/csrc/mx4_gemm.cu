@@ -18,8 +18,8 @@
 // overwritten only after the MMAs that read them released the stage.
 //
 // Persistent, one CTA per SM, roles as in gemm.cu: the producer is a lone
-// thread in a last warp, lane 0 of warp 1 issues the copies to TMEM and the
-// MMAs, warps 2..9 are the epilogue.  Every wait is bounded.
+// thread in a last warp, warp 1 issues the copies to TMEM and the MMAs, warps
+// 2..9 are the epilogue.  Every wait is bounded.
 #include <algorithm>
 
 #include "gemm_common.cuh"
@@ -166,45 +166,50 @@ __global__ void __maxnreg__(kGemmRegs)
   } else if (warp == 0) {
     // idle
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ---------------- MMA issuer ----------------
-      uint32_t s = 0, ph = 0;
-      bool ok = true;
-      for (int i = 0; ok && i < my_tiles; ++i) {
-        const uint32_t b = i & 1, bph = (i >> 1) & 1;
-        if (!mbar_wait(&tempty[b], bph ^ 1, abort_flag, args.status)) {
-          ok = false;
-          break;
-        }
+    // ---------------- MMA issuer: the warp waits, one elected lane issues ----
+    const bool lead = elect_one();
+    const uint64_t a_desc0 = sw128_kmajor_desc(smem), sc_desc0 = mx4_scale_desc(smem);
+    uint32_t s = 0, ph = 0;
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+      return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, args.status)) != 0;
+    };
+    for (int i = 0; ok && i < my_tiles; ++i) {
+      const uint32_t b = i & 1, bph = (i >> 1) & 1;
+      ok = wait(&tempty[b], bph ^ 1);
+      if (!ok) break;
+      const uint32_t d_tmem = tmem_base + b * kMxBN;
+      for (int k = 0; k < kt; ++k) {
+        ok = wait(&full[s], ph);
+        if (!ok) break;
         tc_fence_after();
-        const uint32_t d_tmem = tmem_base + b * kMxBN;
-        for (int k = 0; k < kt; ++k) {
-          if (!mbar_wait(&full[s], ph, abort_flag, args.status)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint8_t *sa = smem + s * kMxStageBytes, *sw = sa + kMxTileBytes;
+        if (lead) {
+          // (a descriptor's address field is the shared-memory address / 16)
+          const uint64_t at = (uint64_t)(s * (kMxStageBytes >> 4));
+          const uint64_t a_desc = a_desc0 + at, sc_desc = sc_desc0 + at;
           const uint32_t sfa = tmem_base + kScaleBase + s * kScaleCols, sfb = sfa + 8;
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
-            copy_scales(sfa + 4 * g, mx4_scale_desc(sa + kMxCodeBytes + g * kMxGroupBytes));
-            copy_scales(sfb + 4 * g, mx4_scale_desc(sw + kMxCodeBytes + g * kMxGroupBytes));
+            copy_scales(sfa + 4 * g, sc_desc + ((kMxCodeBytes + g * kMxGroupBytes) >> 4));
+            copy_scales(sfb + 4 * g, sc_desc + ((kMxTileBytes + kMxCodeBytes + g * kMxGroupBytes) >> 4));
           }
-          const uint64_t a_desc = sw128_kmajor_desc(sa), b_desc = sw128_kmajor_desc(sw);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            mma_mx4(d_tmem, a_desc + 2 * j, b_desc + 2 * j, kIdesc | ((j & 1) ? kMxSecondPair : 0u),
-                    sfa + 4 * (j >> 1), sfb + 4 * (j >> 1), (k | j) != 0);
+            mma_mx4(d_tmem, a_desc + 2 * j, a_desc + ((kMxTileBytes >> 4) + 2 * j),
+                    kIdesc | ((j & 1) ? kMxSecondPair : 0u), sfa + 4 * (j >> 1), sfb + 4 * (j >> 1),
+                    (k | j) != 0);
           mma_commit(&empty[s]);
-          if (++s == (uint32_t)kMxStages) {
-            s = 0;
-            ph ^= 1;
-          }
         }
-        if (ok) mma_commit(&tfull[b]);
+        __syncwarp();
+        if (++s == (uint32_t)kMxStages) {
+          s = 0;
+          ph ^= 1;
+        }
       }
-      // nothing of this CTA is in flight when it leaves (bounded)
+      if (ok && lead) mma_commit(&tfull[b]);
+      __syncwarp();
+    }
+    if (lead) {  // nothing of this CTA is in flight when it leaves (bounded)
       mma_commit(mma_done);
       volatile int no_abort = 0;
       (void)mbar_wait_bounded(mma_done, 0, &no_abort, args.status);

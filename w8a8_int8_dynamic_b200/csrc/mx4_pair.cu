@@ -13,9 +13,10 @@
 // [0, 256) and [192, 448), which leaves [448, 496) for two sets of scales.  The
 // epilogue drains the shared 64 columns first (each of the two warps of a lane
 // quarter 32 of them) and reports them on a barrier of their own: the next
-// tile's MMAs start one chunk into the epilogue, not after it.  A set of
-// scales is written again only when the MMAs that read it, two steps before,
-// have completed.
+// tile's MMAs start one chunk into the epilogue, not after it.  The
+// copies of scales and the MMAs of one thread execute in the order of their
+// issue; with two sets in turn a copy need not wait for the MMAs just before
+// it.
 //
 // Persistent clusters of two CTAs, roles as in gemm2sm.cu.  No load uses
 // multicast.  Every wait is bounded; a pair that gives up meets at the cluster
@@ -173,60 +174,62 @@ __global__ void __maxnreg__(kGemmRegs)
         (void)mbar_wait_bounded(&full[sl], (uint32_t)((last / S) & 1), &no_abort, args.status);
       }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       // ---------------- MMA issuer (even CTA) ----------------
-      uint32_t s = 0, ph = 0;       // stage of this step
-      uint32_t s2 = 0, ph2 = 0;     // stage of two steps before
-      int64_t step = 0;
+      // The whole warp walks the steps and waits; one elected lane issues.
+      const bool lead = elect_one();
+      const uint64_t a_desc0 = sw128_kmajor_desc(smem), sc_desc0 = mx4_scale_desc(smem);
+      const uint32_t sf0 = tmem_base + kScaleBase;
+      uint32_t s = 0, ph = 0, step = 0;
       bool ok = true;
+      auto wait = [&](uint64_t *bar, uint32_t parity) {
+        return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, args.status)) != 0;
+      };
       for (int i = 0; ok && i < my_tiles; ++i) {
         const uint32_t b = i & 1, bph = (i >> 1) & 1;
         // the accumulator's previous tile is drained, and of the other
         // accumulator's tile the columns they share
-        if (!mbar_wait(&tempty[b], bph ^ 1, abort_flag, args.status) ||
-            (i > 0 && !mbar_wait(&tshared[b ^ 1], ((i - 1) >> 1) & 1, abort_flag, args.status))) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
+        ok = wait(&tempty[b], bph ^ 1) && (i == 0 || wait(&tshared[b ^ 1], ((i - 1) >> 1) & 1));
+        if (!ok) break;
         const uint32_t d_tmem = tmem_base + acc_col(b);
         for (int k = 0; k < kt; ++k, ++step) {
-          if (!mbar_wait(&full[s], ph, abort_flag, args.status) ||
-              (step >= (int64_t)kScaleSets && !mbar_wait(&empty[s2], ph2, abort_flag, args.status))) {
-            ok = false;
-            break;
-          }
-          if (step >= (int64_t)kScaleSets && ++s2 == (uint32_t)S) {
-            s2 = 0;
-            ph2 ^= 1;
-          }
+          ok = wait(&full[s], ph);
+          if (!ok) break;
           tc_fence_after();
-          const uint8_t *st = smem + s * L::kStageBytes;
-          const uint32_t sfa = tmem_base + kScaleBase + (uint32_t)(step & 1) * kScaleSetCols, sfb = sfa + 8;
+          if (lead) {
+            // (a descriptor's address field is the shared-memory address / 16:
+            // one addition a stage, the rest are constants)
+            const uint64_t at = (uint64_t)(s * (L::kStageBytes >> 4));
+            const uint64_t a_desc = a_desc0 + at, sc_desc = sc_desc0 + at;
+            const uint32_t sfa = sf0 + (step & 1) * kScaleSetCols, sfb = sfa + 8;
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            copy_scales_pair(sfa + 4 * g, mx4_scale_desc(st + kMxCodeBytes + g * kMxGroupBytes));
-            copy_scales_pair(sfb + 8 * g, mx4_scale_desc(st + L::kWS + g * kMxGroupBytes));
-            copy_scales_pair(sfb + 8 * g + 4,
-                             mx4_scale_desc(st + L::kWS + kMxScaleBytes + g * kMxGroupBytes));
+            for (int g = 0; g < 2; ++g) {
+              copy_scales_pair(sfa + 4 * g, sc_desc + ((kMxCodeBytes + g * kMxGroupBytes) >> 4));
+              copy_scales_pair(sfb + 8 * g, sc_desc + ((L::kWS + g * kMxGroupBytes) >> 4));
+              copy_scales_pair(sfb + 8 * g + 4,
+                               sc_desc + ((L::kWS + kMxScaleBytes + g * kMxGroupBytes) >> 4));
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              mma_mx4_pair(d_tmem, a_desc + 2 * j, a_desc + ((L::kW >> 4) + 2 * j),
+                           kIdesc | ((j & 1) ? kMxSecondPair : 0u), sfa + 4 * (j >> 1), sfb + 8 * (j >> 1),
+                           (k | j) != 0);
+            mma_commit_pair(&empty[s], 0x3);
           }
-          const uint64_t a_desc = sw128_kmajor_desc(st), b_desc = sw128_kmajor_desc(st + L::kW);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mma_mx4_pair(d_tmem, a_desc + 2 * j, b_desc + 2 * j,
-                         kIdesc | ((j & 1) ? kMxSecondPair : 0u), sfa + 4 * (j >> 1), sfb + 8 * (j >> 1),
-                         (k | j) != 0);
-          mma_commit_pair(&empty[s], 0x3);
+          __syncwarp();
           if (++s == (uint32_t)S) {
             s = 0;
             ph ^= 1;
           }
         }
-        if (ok) mma_commit_pair(&tfull[b], 0x3);
+        if (ok && lead) mma_commit_pair(&tfull[b], 0x3);
+        __syncwarp();
       }
-      mma_commit_pair(mma_done, 0x1);  // nothing in flight when the pair leaves (bounded)
-      volatile int no_abort = 0;
-      (void)mbar_wait_bounded(mma_done, 0, &no_abort, args.status);
+      if (lead) {  // nothing in flight when the pair leaves (bounded)
+        mma_commit_pair(mma_done, 0x1);
+        volatile int no_abort = 0;
+        (void)mbar_wait_bounded(mma_done, 0, &no_abort, args.status);
+      }
     }
     __syncwarp();
   } else if (warp >= 2 && threadIdx.x < kGemmThreads) {

@@ -201,41 +201,42 @@ __global__ void __launch_bounds__(kStreamThreads + (QUANT ? 32 * kQuantWarps : 0
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ---------------- MMA issuer ----------------
-      uint32_t s = 0, ph = 0, seg = 0;
-      bool ok = true;
-      int64_t u = u_begin;
-      while (ok && u < u_end) {
-        const int64_t nb = u / nku;
-        const int64_t seg_end = min(u_end, (nb + 1) * nku);
-        const uint32_t b = seg & 1, bph = (seg >> 1) & 1;
-        if (!mbar_wait(&tempty[b], bph ^ 1, abort_flag, args.p.status)) {
-          ok = false;
-          break;
-        }
+    // ---------------- MMA issuer: the warp waits, one elected lane issues ----
+    const bool lead = elect_one();
+    const uint64_t desc0 = sw128_kmajor_desc(smem), sc_desc0 = mx4_scale_desc(smem);
+    uint32_t s = 0, ph = 0, seg = 0;
+    bool ok = true;
+    int64_t u = u_begin;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+      return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, args.p.status)) != 0;
+    };
+    while (ok && u < u_end) {
+      const int64_t nb = u / nku;
+      const int64_t seg_end = min(u_end, (nb + 1) * nku);
+      const uint32_t b = seg & 1, bph = (seg >> 1) & 1;
+      ok = wait(&tempty[b], bph ^ 1);
+      if (!ok) break;
+      const uint32_t d_tmem = tmem_base + b * NT;
+      uint32_t acc = 0;
+      for (int k0 = (int)(u - nb * nku) * kUnitTiles; u < seg_end; ++u, k0 += kUnitTiles) {
+        ok = wait(&full[s], ph);
+        if (!ok) break;
         tc_fence_after();
-        const uint32_t d_tmem = tmem_base + b * NT;
-        uint32_t acc = 0;
-        for (int k0 = (int)(u - nb * nku) * kUnitTiles; u < seg_end; ++u, k0 += kUnitTiles) {
-          if (!mbar_wait(&full[s], ph, abort_flag, args.p.status)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint8_t *st = smem + s * L::kStageBytes;
+        if (lead) {
+          // (a descriptor's address field is the shared-memory address / 16)
+          const uint64_t at = (uint64_t)(s * (L::kStageBytes >> 4));
           const int nk = min(kUnitTiles, kt - k0);
           for (int h = 0; h < nk; ++h) {
-            const uint8_t *sw = st + L::kW + h * kMxTileBytes;
-            const uint8_t *ss = st + L::kS + h * kMxScaleBytes;
+            const uint64_t wd = desc0 + at + (uint64_t)(h * (kMxTileBytes >> 4));
+            const uint64_t qd = desc0 + at + (uint64_t)((L::kQ + h * L::kCodes) >> 4);
+            const uint64_t ws = sc_desc0 + at + (uint64_t)((h * kMxTileBytes + kMxCodeBytes) >> 4);
+            const uint64_t qs = sc_desc0 + at + (uint64_t)((L::kS + h * kMxScaleBytes) >> 4);
             const uint32_t sfw = tmem_base + 2 * NT + s * L::kScaleCols + h * 16, sfq = sfw + 8;
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
-              copy_scales(sfw + 4 * g, mx4_scale_desc(sw + kMxCodeBytes + g * kMxGroupBytes));
-              copy_scales(sfq + 4 * g, mx4_scale_desc(ss + g * kMxGroupBytes));
+              copy_scales(sfw + 4 * g, ws + ((g * kMxGroupBytes) >> 4));
+              copy_scales(sfq + 4 * g, qs + ((g * kMxGroupBytes) >> 4));
             }
-            const uint64_t wd = sw128_kmajor_desc(sw);
-            const uint64_t qd = sw128_kmajor_desc(st + L::kQ + h * L::kCodes);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               mma_mx4(d_tmem, wd + 2 * j, qd + 2 * j, kIdesc | ((j & 1) ? kMxSecondPair : 0u),
@@ -244,15 +245,20 @@ __global__ void __launch_bounds__(kStreamThreads + (QUANT ? 32 * kQuantWarps : 0
             }
           }
           mma_commit(&empty[s]);
-          if (++s == (uint32_t)S) {
-            s = 0;
-            ph ^= 1;
-          }
         }
-        if (ok) mma_commit(&tfull[b]);
-        ++seg;
+        acc = 1;
+        __syncwarp();
+        if (++s == (uint32_t)S) {
+          s = 0;
+          ph ^= 1;
+        }
       }
-      mma_commit(mma_done);  // nothing of this CTA is in flight when it leaves (bounded)
+      if (ok && lead) mma_commit(&tfull[b]);
+      __syncwarp();
+      ++seg;
+    }
+    if (lead) {  // nothing of this CTA is in flight when it leaves (bounded)
+      mma_commit(mma_done);
       volatile int no_abort = 0;
       (void)mbar_wait_bounded(mma_done, 0, &no_abort, args.p.status);
     }

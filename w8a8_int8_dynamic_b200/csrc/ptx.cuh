@@ -207,6 +207,15 @@ __device__ __forceinline__ void griddep_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// One lane of a converged warp (the same one on every call).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // ---- tcgen05 -------------------------------------------------------------------
 // Allocation is warp-wide; the TMEM base address is written to *slot (shared).
 __device__ __forceinline__ void tmem_alloc(uint32_t *slot, uint32_t ncols) {
