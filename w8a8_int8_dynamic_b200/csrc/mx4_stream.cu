@@ -15,9 +15,9 @@
 // usually does) reads their partials while its own MMAs run.
 //
 // QUANT (the layer, M <= 16): x comes as bf16 and four more warps form its
-// codes and scales, one block of 32 a thread, straight into the pipeline
+// codes and scales, a block of 32 in one lane, straight into the pipeline
 // stage: no quantisation launch, no image of x in memory.  Each CTA forms the
-// tiles that its units need; the next unit's loads are in flight meanwhile.
+// tiles that its units need.
 //
 // Before the wait for the preceding kernel of the stream, whose output x (or
 // even the weights) may be, the first weight units are only asked into L2,
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kStreamThreads + (QUANT ? 32 * kQuantWarps : 0
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], QUANT ? 1 + kQuantWarps : 1);
+      mbar_init(&full[s], QUANT ? 2 : 1);  // the copies; the codes of x
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -305,6 +305,28 @@ __global__ void __launch_bounds__(kStreamThreads + (QUANT ? 32 * kQuantWarps : 0
         if (in) args.counters[nb] = 0ull;
         return in;
       };
+      // Adds the partials of contributors hi, hi - 1, ..., lo + 1 in that order
+      // (chunk c), the loads of kGroup of them in flight together: one after
+      // another they cost a round trip to L2 each, at the kernel's tail
+      // (13 x 5120 x 13824, 5 contributors a slab: 7 us of 16.6 us).
+      constexpr int kGroup = kChunk == 16 ? 4 : 2;
+      auto add_parts = [&](float (&sum)[kChunk], int hi, int lo, int c) {
+        const float *base = slots + c * kChunk * 128;
+        for (int o = hi; o > lo; o -= kGroup) {
+          float v[kGroup][kChunk];
+#pragma unroll
+          for (int g = 0; g < kGroup; ++g)
+#pragma unroll
+            for (int m = 0; m < kChunk; ++m)
+              v[g][m] = o - g > lo ? __ldcg(base + (size_t)(o - g) * (128 * NT) + m * 128) : 0.0f;
+#pragma unroll
+          for (int g = 0; g < kGroup; ++g)
+            if (o - g > lo) {
+#pragma unroll
+              for (int m = 0; m < kChunk; ++m) sum[m] += v[g][m];
+            }
+        }
+      };
       // While this CTA's MMAs run: the later contributors' partials, if all are in.
       bool finish = whole;
       float pre[kChunk];
@@ -315,11 +337,7 @@ __global__ void __launch_bounds__(kStreamThreads + (QUANT ? 32 * kQuantWarps : 0
           have_pre = true;
 #pragma unroll
           for (int m = 0; m < kChunk; ++m) pre[m] = 0.0f;
-          for (int c = contributors - 1; c > rank; --c) {
-            const float *o = slots + (size_t)c * (128 * NT);
-#pragma unroll
-            for (int m = 0; m < kChunk; ++m) pre[m] += __ldcg(o + m * 128);
-          }
+          add_parts(pre, contributors - 1, rank, 0);
         }
       }
       if (!decide(2 + b, et == 0 ? (mbar_wait(&tfull[b], bph, abort_flag, args.p.status) ? 1 : 0) : 0)) break;
@@ -366,21 +384,11 @@ __global__ void __launch_bounds__(kStreamThreads + (QUANT ? 32 * kQuantWarps : 0
           if (!whole) {
             float sum[kChunk];
 #pragma unroll
-            for (int m = 0; m < kChunk; ++m) sum[m] = 0.0f;
-            if (have_pre) {
+            for (int m = 0; m < kChunk; ++m) sum[m] = have_pre ? pre[m] : 0.0f;
+            if (!have_pre) add_parts(sum, contributors - 1, rank, c);
 #pragma unroll
-              for (int m = 0; m < kChunk; ++m) sum[m] = pre[m];
-            }
-            for (int o = have_pre ? rank : contributors - 1; o >= 0; --o) {
-              if (o == rank) {
-#pragma unroll
-                for (int m = 0; m < kChunk; ++m) sum[m] += r[m];
-              } else {
-                const float *p = slots + (size_t)o * (128 * NT) + c * kChunk * 128;
-#pragma unroll
-                for (int m = 0; m < kChunk; ++m) sum[m] += __ldcg(p + m * 128);
-              }
-            }
+            for (int m = 0; m < kChunk; ++m) sum[m] += r[m];
+            add_parts(sum, rank - 1, -1, c);
 #pragma unroll
             for (int m = 0; m < kChunk; ++m) r[m] = sum[m];
           }
@@ -438,54 +446,57 @@ __global__ void __launch_bounds__(kStreamThreads + (QUANT ? 32 * kQuantWarps : 0
       ++seg;
     }
   } else if (QUANT) {
-    // ---------------- quantisation (warps 6..9): one block per thread ----------
+    // ---------------- quantisation (warps 6..9): every fourth unit a warp -------
+    // A unit is 16 blocks of each row: a lane takes block lane & 15 of every
+    // second row.  The loads of up to eight rows are in flight together, and a
+    // warp has the time of four units for its one (with all four warps on
+    // every unit, each paid a round trip to L2: slower than the weights).
     griddep_wait();
-    const int t = threadIdx.x - kStreamThreads;
-    const int row = t >> 3, blk = t & 7;  // 16 rows x 8 blocks of a tile
-    const bool mine = row < args.p.M;
-    const uint16_t *xr = args.x + (int64_t)row * args.ldx + blk * 32;
-    struct Loaded {
-      uint4 v[kUnitTiles][4];
-    };
-    auto fetch = [&](int k0, Loaded &d) {
-#pragma unroll
-      for (int h = 0; h < kUnitTiles; ++h)
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int k = (k0 + h) * kMxTileK + blk * 32 + g * 8;
-          d.v[h][g] = make_uint4(0, 0, 0, 0);
-          if (mine && k < args.K)
-            d.v[h][g] = *reinterpret_cast<const uint4 *>(xr + (k0 + h) * kMxTileK + g * 8);
-        }
-    };
+    const int qw = warp - kStreamThreads / 32;
+    const int M = args.p.M, blk = lane & 7, h = (lane >> 3) & 1;
     const int nb0 = (int)(u_begin / nku);
     int k0 = (int)(u_begin - (int64_t)nb0 * nku) * kUnitTiles;
-    auto after = [&](int k) { return kt - k <= kUnitTiles ? 0 : k + kUnitTiles; };
-    Loaded cur, ahead;
-    if (n_units > 0) fetch(k0, cur);
-    uint32_t s = 0, ph = 0;
-    for (int64_t i = 0; i < n_units; ++i) {
-      const int k1 = after(k0);
-      if (i + 1 < n_units) fetch(k1, ahead);
-      if (i >= S) {  // the stage's previous MMAs are done
-        int ok = 0;
-        if (lane == 0) ok = mbar_wait(&empty[s], ph ^ 1, abort_flag, args.p.status);
-        if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
-      }
-      uint8_t *st = smem + s * L::kStageBytes;
+    uint32_t s = 0, ph = 0;  // the ring's first round needs no wait
+    bool ok = true;
+    constexpr int kRows = 4;  // rows of a lane in flight
+    for (int64_t i = 0; ok && i < n_units; ++i) {
+      if ((int)(i & (kQuantWarps - 1)) == qw) {
+        uint8_t *st = smem + s * L::kStageBytes;
+        const int k = (k0 + h) * kMxTileK + blk * 32;
+        const bool in_tile = k0 + h < kt;
+        for (int r0 = lane >> 4; r0 < M || r0 < 2; r0 += 2 * kRows) {
+          uint4 v[kRows][4];
 #pragma unroll
-      for (int h = 0; h < kUnitTiles; ++h) {
-        if (k0 + h >= kt || !mine) continue;
-        uint4 codes;
-        const uint32_t c = mx4_encode_block(cur.v[h], codes);
-        *reinterpret_cast<uint4 *>(st + L::kQ + h * L::kCodes + mx4_chunk_offset(row, blk)) = codes;
-        st[L::kS + h * kMxScaleBytes + mx4_scale_offset(row, blk) - kMxCodeBytes] = (uint8_t)c;
+          for (int j = 0; j < kRows; ++j)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              const int row = r0 + 2 * j;
+              v[j][g] = make_uint4(0, 0, 0, 0);
+              if (row < M && k + g * 8 < args.K)
+                v[j][g] = *reinterpret_cast<const uint4 *>(args.x + (int64_t)row * args.ldx + k + g * 8);
+            }
+          if (r0 < 2 && i >= S) {  // the stage's previous MMAs are done
+            int done = 0;
+            if (lane == 0) done = mbar_wait(&empty[s], ph ^ 1, abort_flag, args.p.status);
+            ok = __shfl_sync(0xFFFFFFFFu, done, 0) != 0;
+            if (!ok) break;
+          }
+#pragma unroll
+          for (int j = 0; j < kRows; ++j) {
+            const int row = r0 + 2 * j;
+            if (row >= M || !in_tile) continue;
+            uint4 codes;
+            const uint32_t c = mx4_encode_block(v[j], codes);
+            *reinterpret_cast<uint4 *>(st + L::kQ + h * L::kCodes + mx4_chunk_offset(row, blk)) = codes;
+            st[L::kS + h * kMxScaleBytes + mx4_scale_offset(row, blk) - kMxCodeBytes] = (uint8_t)c;
+          }
+        }
+        if (!ok) break;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[s]);
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&full[s]);
-      cur = ahead;
-      k0 = k1;
+      k0 = kt - k0 <= kUnitTiles ? 0 : k0 + kUnitTiles;
       if (++s == (uint32_t)S) {
         s = 0;
         ph ^= 1;
