@@ -337,25 +337,23 @@ w8a8_status w8a8_mx4_dequant(const void *image, int64_t rows, int64_t K, void *x
                              w8a8_stream_t stream);
 
 /* y (device, bf16 [M, N]) from the images of [M, K] and [N, K]; bias (device,
- * bf16 [N]) or NULL; act: a w8a8_act.  workspace: device scratch of ws_bytes
- * >= w8a8_mx4_scaled_mm_workspace_bytes (NULL where that is 0); its contents
- * on entry do not matter.  Calls that share one must not overlap. */
-w8a8_status w8a8_mx4_scaled_mm_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t *bytes);
+ * bf16 [N]) or NULL; act: a w8a8_act.  No workspace. */
 w8a8_status w8a8_mx4_scaled_mm(const void *a_image, const void *w_image, const void *bias, void *y,
-                               int64_t M, int64_t N, int64_t K, int act, void *workspace,
-                               size_t ws_bytes, w8a8_stream_t stream);
+                               int64_t M, int64_t N, int64_t K, int act, w8a8_stream_t stream);
 
 /* The same product, with the image of y in place of y: equal, bit for bit, to
  * w8a8_mx4_quant of the y of w8a8_mx4_scaled_mm.  The codes are formed in the
  * epilogue; y does not reach memory.  y_image_bytes >= w8a8_mx4_bytes(M, N). */
 w8a8_status w8a8_mx4_scaled_mm_quant(const void *a_image, const void *w_image, const void *bias,
                                      void *y_image, size_t y_image_bytes, int64_t M, int64_t N,
-                                     int64_t K, int act, void *workspace, size_t ws_bytes,
-                                     w8a8_stream_t stream);
+                                     int64_t K, int act, w8a8_stream_t stream);
 
 /* The whole layer: quantisation of x, then the product as a programmatic
- * dependent of it.  workspace (never NULL): the image of x, then the
- * product's workspace. */
+ * dependent of it; up to 16 rows one kernel does both.  The result is that of
+ * w8a8_mx4_quant and w8a8_mx4_scaled_mm, bit for bit.  workspace: the image of
+ * x, ws_bytes >= w8a8_mx4_linear_workspace_bytes (NULL where that is 0: M <=
+ * 16); its contents on entry do not matter, and calls that share one must not
+ * overlap. */
 w8a8_status w8a8_mx4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t *bytes);
 w8a8_status w8a8_mx4_linear(const void *x, int64_t ldx, const void *w_image, const void *bias, void *y,
                             int64_t M, int64_t N, int64_t K, int act, void *workspace, size_t ws_bytes,

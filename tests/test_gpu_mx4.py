@@ -160,22 +160,28 @@ def test_product_with_codes_of_its_output(M, N, K, act):
 
 
 @pytest.mark.parametrize("path", [w8.PATH_LARGE, w8.PATH_SMALL])
-@pytest.mark.parametrize("M,N,K", [(1, 1000, 5120), (4, 520, 13824), (16, 4096, 1040), (16, 136, 8208),
-                                   (17, 4096, 528), (64, 2056, 4112), (128, 1032, 2064), (100, 8, 16384)])
+@pytest.mark.parametrize("M,N,K", [(1, 1000, 5120), (4, 520, 13824), (16, 4096, 1040), (16, 136, 8208), (13, 5120, 784),
+                                   (17, 4096, 528), (30, 136, 13824), (64, 2056, 4112), (50, 8, 16384),
+                                   (33, 27648, 272)])
 def test_product_of_few_rows_on_either_path(M, N, K, path):
-    """Slabs of one and of many contributors, short and long K: both kernels, twice, y and its codes."""
+    """One and several slabs a cluster, K whole and split in up to eight: both kernels, y and its codes."""
     x, w, b = operands(M + N + K, M, N, K)
     a = w8.mx4_quant(x)
     w8.set_path(path)
     try:
-        y = w8.mx4_linear(x, w, b)
+        y = w8.mx4_scaled_mm(a, w, b)
         check_product(y, a, w, b, w8.ACT_NONE)
-        for _ in range(5):  # the same bits, whoever finishes a slab
-            assert torch.equal(w8.mx4_linear(x, w, b), y)
+        for _ in range(5):
             assert torch.equal(w8.mx4_scaled_mm(a, w, b), y)
+        if path == w8.PATH_SMALL or M > 16:
+            assert torch.equal(w8.mx4_linear(x, w, b), y)
         if N % 16 == 0:
-            t = w8.mx4_linear_quant(x, w, b)
-            assert all(torch.equal(g, v) for g, v in zip(t.unpack(), w8.mx4_quant(y).unpack()))
+            image = torch.full((w8.mx4_bytes(M, N),), 0xFF, dtype=torch.uint8, device="cuda")
+            t = w8.mx4_scaled_mm_quant(a, w, b, image=image)
+            want, padded = w8.mx4_quant(y), -(-N // 256) * 256
+            for g, v in zip(w8.MX4Tensor(t.image, (128,), padded).unpack(), w8.MX4Tensor(want.image, (M,), padded).unpack()):
+                assert torch.equal(g[:M], v)
+                assert (g[M:] == 0xFF).all()  # the rows behind are left alone
     finally:
         w8.set_path(w8.PATH_AUTO)
 

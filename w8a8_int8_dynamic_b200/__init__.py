@@ -15,6 +15,5 @@ from .binding import (  # noqa: F401
     set_path, unpack_weight)
 from .mx4 import (  # noqa: F401
     MX4Linear, MX4Tensor, mx4_bytes, mx4_dequant, mx4_linear, mx4_linear_quant,
-    mx4_linear_workspace_bytes, mx4_pack, mx4_quant, mx4_scaled_mm, mx4_scaled_mm_quant,
-    mx4_scaled_mm_workspace_bytes, mx4_unpack)
+    mx4_linear_workspace_bytes, mx4_pack, mx4_quant, mx4_scaled_mm, mx4_scaled_mm_quant, mx4_unpack)
 from .norms import BlockNormOutput, Norm, block_norm  # noqa: F401

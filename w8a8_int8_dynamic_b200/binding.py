@@ -75,10 +75,8 @@ _SIGNATURES = {
     "w8a8_mx4_pack": ([_P, _P, _I64, _I64, _P, _SZ, _P], ctypes.c_int),
     "w8a8_mx4_unpack": ([_P, _I64, _I64, _P, _P, _P], ctypes.c_int),
     "w8a8_mx4_dequant": ([_P, _I64, _I64, _P, _P], ctypes.c_int),
-    "w8a8_mx4_scaled_mm_workspace_bytes": ([_I64, _I64, _I64, ctypes.POINTER(_SZ)], ctypes.c_int),
-    "w8a8_mx4_scaled_mm": ([_P, _P, _P, _P, _I64, _I64, _I64, ctypes.c_int, _P, _SZ, _P],
-                           ctypes.c_int),
-    "w8a8_mx4_scaled_mm_quant": ([_P, _P, _P, _P, _SZ, _I64, _I64, _I64, ctypes.c_int, _P, _SZ, _P],
+    "w8a8_mx4_scaled_mm": ([_P, _P, _P, _P, _I64, _I64, _I64, ctypes.c_int, _P], ctypes.c_int),
+    "w8a8_mx4_scaled_mm_quant": ([_P, _P, _P, _P, _SZ, _I64, _I64, _I64, ctypes.c_int, _P],
                                  ctypes.c_int),
     "w8a8_mx4_linear_workspace_bytes": ([_I64, _I64, _I64, ctypes.POINTER(_SZ)], ctypes.c_int),
     "w8a8_mx4_linear": ([_P, _I64, _P, _P, _P, _I64, _I64, _I64, ctypes.c_int, _P, _SZ, _P],

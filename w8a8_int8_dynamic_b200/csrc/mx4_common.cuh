@@ -91,6 +91,18 @@ __device__ __forceinline__ uint32_t mx4_codes8(float v0, float v1, float v2, flo
   return r;
 }
 
+// One value of a block with scale code c -> its code.
+__device__ __forceinline__ uint32_t mx4_code1(float v, uint32_t c) {
+  if (c == 255u) return 0u;
+  uint32_t r;
+  asm("{\n\t.reg .b8 b, z;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\t"
+      "mov.b32 %0, {b, z, z, z};\n\t}"
+      : "=r"(r)
+      : "f"(v * mx4_inverse_scale(c)), "f"(0.0f));
+  return r & 15u;
+}
+
 // Eight bf16 values (four packed pairs) of a block with scale code c -> codes.
 __device__ __forceinline__ uint32_t mx4_encode8(const uint4 &x, uint32_t c) {
   if (c == 255u) return 0u;
@@ -201,10 +213,8 @@ struct Mx4Args {
 
 // Few rows (mx4_stream.cu), M <= kStreamRows.  x: bf16 rows that the kernel
 // quantises itself (M <= kStreamQuantRows), or null: p.a is their image.
-constexpr int64_t kStreamRows = 128, kStreamQuantRows = 16;
-int64_t mx4_stream_workspace_bytes(int64_t M, int64_t N, int64_t K);
-w8a8_status launch_mx4_stream(const Mx4Args &p, const void *x, int64_t ldx, int64_t K, void *workspace,
-                              cudaStream_t stream);
+constexpr int64_t kStreamRows = 64, kStreamQuantRows = 16;
+w8a8_status launch_mx4_stream(const Mx4Args &p, const void *x, int64_t ldx, int64_t K, cudaStream_t stream);
 
 // Many rows (mx4_pair.cu): 256 x 256 tiles on CTA pairs.
 w8a8_status launch_mx4_pair(Mx4Args a, cudaStream_t stream);

@@ -319,7 +319,7 @@ w8a8_status launch_mx4_1sm(const CUtensorMap &ty, Mx4Args a, cudaStream_t stream
   return from_cuda(e);
 }
 
-// Up to 128 rows the weight stream sets the time (mx4_stream.cu).
+// Up to 64 rows the weight stream sets the time (mx4_stream.cu).
 bool use_stream(int64_t M) {
   const int p = forced_path();
   return M <= kStreamRows && (p == 0 || p == 2);
@@ -335,8 +335,8 @@ bool use_pair(const Mx4Args &a) {
 
 // x (with ldx; a layer of few rows): quantised by the product itself, in place of a_image.
 w8a8_status launch_mx4(const void *a_image, const void *w_image, const void *bias, void *y,
-                       void *y_image, int64_t M, int64_t N, int64_t K, int act, void *workspace,
-                       const void *x, int64_t ldx, cudaStream_t stream) {
+                       void *y_image, int64_t M, int64_t N, int64_t K, int act, const void *x,
+                       int64_t ldx, cudaStream_t stream) {
   Mx4Args a{};
   a.a = static_cast<const uint8_t *>(a_image);
   a.w = static_cast<const uint8_t *>(w_image);
@@ -351,7 +351,7 @@ w8a8_status launch_mx4(const void *a_image, const void *w_image, const void *bia
   a.status = status_word();
   if (!a.status) return W8A8_ERR_CUDA;
   if (forced_path() == 2 && M > kStreamRows) return W8A8_ERR_INVALID_ARG;
-  if (use_stream(M)) return launch_mx4_stream(a, x, ldx, K, workspace, stream);
+  if (x || use_stream(M)) return launch_mx4_stream(a, x, ldx, K, stream);
   if (use_pair(a)) return launch_mx4_pair(a, stream);
   CUtensorMap ty = {};
   if (y && !make_tmap_out_bf16(&ty, y, (uint64_t)M, (uint64_t)N)) return W8A8_ERR_CUDA;
@@ -372,52 +372,38 @@ w8a8_status check_product(const void *w_image, const void *bias, const void *y, 
   return W8A8_OK;
 }
 
-int64_t product_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  return M <= kStreamRows ? mx4_stream_workspace_bytes(M, N, K) : 0;
-}
-
 w8a8_status product(const void *a_image, const void *w_image, const void *bias, void *y, void *y_image,
                     size_t y_image_bytes, bool image, int64_t M, int64_t N, int64_t K, int act,
-                    void *workspace, size_t ws_bytes, w8a8_stream_t stream) {
+                    w8a8_stream_t stream) {
   if (!a_image) return W8A8_ERR_INVALID_ARG;
   if (const w8a8_status s = check_product(w_image, bias, y, y_image, image, M, N, K, act)) return s;
-  if (!aligned16(a_image) || (workspace && !aligned16(workspace))) return W8A8_ERR_ALIGNMENT;
-  if ((image && y_image_bytes < (size_t)mx4_image_bytes(M, N)) ||
-      (workspace ? ws_bytes : 0) < (size_t)product_workspace_bytes(M, N, K))
-    return W8A8_ERR_BUFFER_TOO_SMALL;
+  if (!aligned16(a_image)) return W8A8_ERR_ALIGNMENT;
+  if (image && y_image_bytes < (size_t)mx4_image_bytes(M, N)) return W8A8_ERR_BUFFER_TOO_SMALL;
   return launch_mx4(a_image, w_image, bias, image ? nullptr : y, image ? y_image : nullptr, M, N, K,
-                    act, workspace, nullptr, 0, reinterpret_cast<cudaStream_t>(stream));
+                    act, nullptr, 0, reinterpret_cast<cudaStream_t>(stream));
 }
 
-// A layer's workspace: the image of x, then the product's.
-int64_t layer_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  return round_up(mx4_image_bytes(M, K), 256) + product_workspace_bytes(M, N, K);
+// A layer's workspace: the image of x, which up to 16 rows the product forms
+// itself (whatever path is set).
+int64_t layer_workspace_bytes(int64_t M, int64_t K) {
+  return M <= kStreamQuantRows ? 0 : mx4_image_bytes(M, K);
 }
 
 w8a8_status layer(const void *x, int64_t ldx, const void *w_image, const void *bias, void *y,
                   void *y_image, size_t y_image_bytes, bool image, int64_t M, int64_t N, int64_t K,
                   int act, void *workspace, size_t ws_bytes, w8a8_stream_t stream) {
-  if (!x || !workspace || ldx < K) return W8A8_ERR_INVALID_ARG;
+  if (!x || ldx < K) return W8A8_ERR_INVALID_ARG;
   if (const w8a8_status s = check_product(w_image, bias, y, y_image, image, M, N, K, act)) return s;
   if (!aligned16(x) || ldx % 8 != 0 || !aligned16(workspace)) return W8A8_ERR_ALIGNMENT;
   if ((image && y_image_bytes < (size_t)mx4_image_bytes(M, N)) ||
-      ws_bytes < (size_t)layer_workspace_bytes(M, N, K))
+      (workspace ? ws_bytes : 0) < (size_t)layer_workspace_bytes(M, K))
     return W8A8_ERR_BUFFER_TOO_SMALL;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  uint8_t *ws = static_cast<uint8_t *>(workspace);
-  const int64_t head = round_up(mx4_image_bytes(M, K), 256);
-  const bool fused = use_stream(M) && M <= kStreamQuantRows;
+  const bool fused = M <= kStreamQuantRows;
   if (!fused)
-    if (const w8a8_status r = launch_mx4_quant(x, M, K, ldx, ws, s)) return r;
-  return launch_mx4(ws, w_image, bias, image ? nullptr : y, image ? y_image : nullptr, M, N, K, act,
-                    ws + head, fused ? x : nullptr, ldx, s);
-}
-
-w8a8_status size_query(int64_t M, int64_t N, int64_t K, size_t *bytes, int64_t (*f)(int64_t, int64_t, int64_t)) {
-  if (!bytes || M < 1 || M > 0x7FFFFFFF || N < 1 || N > 0x7FFFFFFF || K < 1) return W8A8_ERR_INVALID_ARG;
-  if (K % 16 != 0 || K > kMaxK || N % 8 != 0) return W8A8_ERR_UNSUPPORTED_SHAPE;
-  *bytes = (size_t)f(M, N, K);
-  return W8A8_OK;
+    if (const w8a8_status r = launch_mx4_quant(x, M, K, ldx, workspace, s)) return r;
+  return launch_mx4(workspace, w_image, bias, image ? nullptr : y, image ? y_image : nullptr, M, N, K, act,
+                    fused ? x : nullptr, ldx, s);
 }
 
 }  // namespace
@@ -427,26 +413,22 @@ using namespace w8a8;
 
 extern "C" {
 
-w8a8_status w8a8_mx4_scaled_mm_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t *bytes) {
-  return size_query(M, N, K, bytes, product_workspace_bytes);
-}
-
 w8a8_status w8a8_mx4_scaled_mm(const void *a_image, const void *w_image, const void *bias, void *y,
-                               int64_t M, int64_t N, int64_t K, int act, void *workspace,
-                               size_t ws_bytes, w8a8_stream_t stream) {
-  return product(a_image, w_image, bias, y, nullptr, 0, false, M, N, K, act, workspace, ws_bytes, stream);
+                               int64_t M, int64_t N, int64_t K, int act, w8a8_stream_t stream) {
+  return product(a_image, w_image, bias, y, nullptr, 0, false, M, N, K, act, stream);
 }
 
 w8a8_status w8a8_mx4_scaled_mm_quant(const void *a_image, const void *w_image, const void *bias,
                                      void *y_image, size_t y_image_bytes, int64_t M, int64_t N,
-                                     int64_t K, int act, void *workspace, size_t ws_bytes,
-                                     w8a8_stream_t stream) {
-  return product(a_image, w_image, bias, nullptr, y_image, y_image_bytes, true, M, N, K, act, workspace,
-                 ws_bytes, stream);
+                                     int64_t K, int act, w8a8_stream_t stream) {
+  return product(a_image, w_image, bias, nullptr, y_image, y_image_bytes, true, M, N, K, act, stream);
 }
 
 w8a8_status w8a8_mx4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t *bytes) {
-  return size_query(M, N, K, bytes, layer_workspace_bytes);
+  if (!bytes || M < 1 || M > 0x7FFFFFFF || N < 1 || N > 0x7FFFFFFF || K < 1) return W8A8_ERR_INVALID_ARG;
+  if (K % 16 != 0 || K > kMaxK || N % 8 != 0) return W8A8_ERR_UNSUPPORTED_SHAPE;
+  *bytes = (size_t)layer_workspace_bytes(M, K);
+  return W8A8_OK;
 }
 
 w8a8_status w8a8_mx4_linear(const void *x, int64_t ldx, const void *w_image, const void *bias, void *y,

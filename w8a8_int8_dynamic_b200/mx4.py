@@ -53,10 +53,6 @@ def mx4_bytes(rows: int, K: int) -> int:
     return _size("w8a8_mx4_bytes", 0, rows, K)
 
 
-def mx4_scaled_mm_workspace_bytes(M: int, N: int, K: int) -> int:
-    return _size("w8a8_mx4_scaled_mm_workspace_bytes", torch.cuda.current_device(), M, N, K)
-
-
 def mx4_linear_workspace_bytes(M: int, N: int, K: int) -> int:
     return _size("w8a8_mx4_linear_workspace_bytes", torch.cuda.current_device(), M, N, K)
 
@@ -207,39 +203,36 @@ def mx4_dequant(t: MX4Tensor, out: Optional[torch.Tensor] = None, stream=None) -
 
 
 def mx4_scaled_mm(a: MX4Tensor, w: MX4Tensor, bias: Optional[torch.Tensor] = None,
-                  out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
-                  stream=None, act: int = ACT_NONE) -> torch.Tensor:
+                  out: Optional[torch.Tensor] = None, stream=None, act: int = ACT_NONE) -> torch.Tensor:
     """The product of a [..., K] with a weight [N, K]: y bf16 [..., N] (``act``: epilogue activation)."""
     _whole(a)
     _weight(w, bias, a.K)
-    index = _device(a.image, w.image, bias, out, workspace)
+    index = _device(a.image, w.image, bias, out)
 
     def f(s):
         M, N, K = a.rows, w.rows, a.K
         y = _output(out, a.lead, N, index)
         if M:
-            ws, nbytes = _scratch(workspace, mx4_scaled_mm_workspace_bytes(M, N, K), index)
             _check(lib().w8a8_mx4_scaled_mm(a.image.data_ptr(), w.image.data_ptr(), _at(bias), y.data_ptr(), M,
-                                            N, K, act, _at(ws), nbytes, s), "w8a8_mx4_scaled_mm")
+                                            N, K, act, s), "w8a8_mx4_scaled_mm")
         return y
     return _call(index, stream, f)
 
 
 def mx4_scaled_mm_quant(a: MX4Tensor, w: MX4Tensor, bias: Optional[torch.Tensor] = None,
-                        image: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
-                        stream=None, act: int = ACT_NONE) -> MX4Tensor:
+                        image: Optional[torch.Tensor] = None, stream=None,
+                        act: int = ACT_NONE) -> MX4Tensor:
     """``mx4_quant(mx4_scaled_mm(...))`` in one kernel: the image of y, the next product's operand."""
     _whole(a)
     _weight(w, bias, a.K)
-    index = _device(a.image, w.image, bias, image, workspace)
+    index = _device(a.image, w.image, bias, image)
 
     def f(s):
         M, N, K = a.rows, w.rows, a.K
         y = _image(image, M, N, index)
         if M:
-            ws, nbytes = _scratch(workspace, mx4_scaled_mm_workspace_bytes(M, N, K), index)
             _check(lib().w8a8_mx4_scaled_mm_quant(a.image.data_ptr(), w.image.data_ptr(), _at(bias),
-                                                  y.data_ptr(), y.numel(), M, N, K, act, _at(ws), nbytes, s),
+                                                  y.data_ptr(), y.numel(), M, N, K, act, s),
                    "w8a8_mx4_scaled_mm_quant")
         return MX4Tensor(y, a.lead, N)
     return _call(index, stream, f)
