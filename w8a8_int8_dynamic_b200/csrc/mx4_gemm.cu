@@ -325,12 +325,23 @@ bool use_stream(int64_t M) {
   return M <= kStreamRows && (p == 0 || p == 2);
 }
 
+// Pairs with 256 x 256 tiles or single CTAs with 128 x 128 ones: by the rounds
+// of tiles, a step of K taking 0.365 us in the one and 0.27 us in the other
+// when all SMs are busy, and 1.4 us more to start and end the pair kernel.
+// Measured (pair, single): 512 x 4096 x 4096 13.1, 10.8 us; 1024 x 4096 x 4096
+// 13.5, 14.8; 256 x 12288 x 4096 13.9, 15.1; 2048^3 11.2, 10.2; 128 x 27648 x
+// 5120 23.4, 20.1; 4096 x 12288 x 4096 77, 99.
 bool use_pair(const Mx4Args &a) {
   const int p = forced_path();
   // (the pair kernel's box coordinates are 32-bit rows of 128 bytes)
   const int64_t most = (std::max(mx4_slabs(a.M), mx4_slabs(a.N)) + 2) * a.kt * (kMxTileBytes / 128);
   if (most > 0x7FFFFFFF || (p != 0 && p != 5 && p != 7)) return false;
-  return p != 0 || ((int64_t)a.M * a.N >= (int64_t)1024 * 4096);
+  if (p != 0) return true;
+  auto rounds = [](int64_t tiles, int64_t slots) { return (double)((tiles + slots - 1) / slots); };
+  const int64_t sms = sm_count();
+  const double pair = rounds(((a.M + 255) / 256) * (int64_t)((a.N + 255) / 256), sms / 2) * a.kt * 0.365 + 1.4;
+  const double single = rounds(mx4_slabs(a.M) * mx4_slabs(a.N), sms) * a.kt * 0.27;
+  return pair < single;
 }
 
 // x (with ldx; a layer of few rows): quantised by the product itself, in place of a_image.

@@ -39,8 +39,8 @@ struct StreamCfg {
   static constexpr int kQ = kMxTileBytes;             // codes of NT rows of x
   static constexpr int kS = kQ + NT * 128;            // their scales
   static constexpr int kStageBytes = kS + kMxScaleBytes;  // a multiple of 1024
-  static constexpr int kRecv = kStages * kStageBytes;  // parts from the cluster's other CTAs
-  static constexpr int kBars = kRecv + 3 * 16 * 128 * 4;  // (C - 1) x ceil(NT / 16 / C) chunks, at most 3
+  static constexpr int kRecv = kStages * kStageBytes;  // the parts of the cluster's CTAs
+  static constexpr int kBars = kRecv + 4 * 16 * 128 * 4;  // C x ceil(NT / 16 / C) chunks: at most 4
   // full[S], empty[S], tfull[2], tempty[2], recv, sent, done
   static constexpr int kMisc = kBars + (2 * kStages + 7) * 8;
   static constexpr int kAlloc = kMisc + 16 + 1024;
@@ -85,6 +85,29 @@ __device__ __forceinline__ bool acquire_cluster(uint64_t *bar, uint32_t parity) 
 }
 __device__ __forceinline__ void arrive_release_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+// One row of a slab's 128 outputs into the image of y: the warp's 32 values
+// (bf16 bits, zero past N) are one block.
+__device__ __noinline__ void image_row(const Mx4Args &p, int row, int nb, int quarter, int lane,
+                                       uint32_t bits) {
+  uint8_t *tile = p.y_image + (size_t)(nb >> 1) * kMxTileBytes;
+  const int blk = (nb & 1) * 4 + quarter;
+  const bool pad = !(nb & 1) && (nb + 1) * 128 >= p.N;  // the tile's other half has no slab
+  const uint32_t code = mx4_scale_code(__reduce_max_sync(0xFFFFFFFFu, bits & 0x7FFFu));
+  uint32_t word = mx4_code1(__uint_as_float(bits << 16), code) << (4 * (lane & 7));
+  word |= __shfl_xor_sync(0xFFFFFFFFu, word, 1);
+  word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2);
+  word |= __shfl_xor_sync(0xFFFFFFFFu, word, 4);
+  if ((lane & 7) == 0) {
+    *reinterpret_cast<uint32_t *>(tile + mx4_chunk_offset(row, blk) + (lane >> 3) * 4) = word;
+    if (pad) *reinterpret_cast<uint32_t *>(tile + mx4_chunk_offset(row, blk + 4) + (lane >> 3) * 4) = 0u;
+  }
+  if (lane == 0) {
+    tile[mx4_scale_offset(row, blk)] = (uint8_t)code;
+    if (pad) tile[mx4_scale_offset(row, blk + 4)] = 0;
+  }
+  __syncwarp();
 }
 
 template <int NT, bool QUANT>
@@ -240,8 +263,9 @@ __global__ void __launch_bounds__(kStreamThreads + (QUANT ? 32 * kQuantWarps : 0
     const int quarter = warp & 3;
     const int n_local = quarter * 32 + lane;
     const int M = args.p.M, N = args.p.N;
-    const int chunks = (M + 15) >> 4;  // 16 rows of x each; chunk q is finished by the CTA of rank q % C
-    // parts[chunk / C][sender, but not own][16][128]
+    // 16 rows of x a chunk; chunk q is finished by the CTA of rank q % C
+    const int chunks = (M + 15) >> 4;
+    // parts[chunk / C][rank][16][128]
     float *parts = reinterpret_cast<float *>(smem + L::kRecv) + n_local;
     const uint32_t parts_addr = smem_addr(parts);
     const uint32_t recv_addr = smem_addr(recv), sent_addr = smem_addr(sent);
@@ -268,7 +292,7 @@ __global__ void __launch_bounds__(kStreamThreads + (QUANT ? 32 * kQuantWarps : 0
           tmem_ld_32x32b_x16(taddr + q * 16, v);
           tmem_ld_wait();
           const uint32_t at = map_to_cta(parts_addr, (uint32_t)to) +
-                              (uint32_t)(((q >> log_c) * (C - 1) + (rank < to ? rank : rank - 1)) * (16 * 512));
+                              (uint32_t)(((q >> log_c) * C + rank) * (16 * 512));
 #pragma unroll
           for (int m = 0; m < 16; ++m)
             if (q * 16 + m < M) st_cluster_f32(at + m * 512, __uint_as_float(v[m]));
@@ -278,69 +302,49 @@ __global__ void __launch_bounds__(kStreamThreads + (QUANT ? 32 * kQuantWarps : 0
         if (lane < C && lane != rank) arrive_release_cluster(map_to_cta(recv_addr, (uint32_t)lane));
         if (!(wait(recv, (uint32_t)i & 1) && acquire_cluster(recv, (uint32_t)i & 1))) break;
       }
+      // Few rows: a short loop, since this code runs once a slab and unrolled
+      // over all 16 rows its instructions take longer to fetch than to execute
+      // (1 x 4096 x 4096: 7.3 us, four rows at a time 6.5).  With more rows the
+      // latencies of a short loop cost more (64 x 27648 x 5120: two rows at a
+      // time 22.7 us, eight 20.0, sixteen 18.2).
       for (int q = rank; q < chunks; q += C) {
-        const int m0 = q * 16;
-        uint32_t v[16];
-        tmem_ld_32x32b_x16(taddr + m0, v);
-        tmem_ld_wait();
-        float t[16];
-        if (C == 1) {
+        const int m0 = q * 16, rows = min(16, M - m0);
+        float *part = parts + (C > 1 ? (q >> log_c) * C : 0) * (16 * 128);
+        {
+          uint32_t v[16];
+          tmem_ld_32x32b_x16(taddr + m0, v);
+          tmem_ld_wait();
 #pragma unroll
-          for (int m = 0; m < 16; ++m) t[m] = __uint_as_float(v[m]);
-        } else {
-          const float *part = parts + (size_t)((q >> log_c) * (C - 1)) * (16 * 128);
-#pragma unroll
-          for (int m = 0; m < 16; ++m) t[m] = 0.0f;
-          for (int r = 0; r < C; ++r) {  // the parts in rank order
-            if (r == rank) {
-#pragma unroll
-              for (int m = 0; m < 16; ++m) t[m] += __uint_as_float(v[m]);
-            } else {
-#pragma unroll
-              for (int m = 0; m < 16; ++m)
-                if (m0 + m < M) t[m] += part[m * 128];
-              part += 16 * 128;
-            }
-          }
+          for (int m = 0; m < 16; ++m)
+            if (m < rows) part[(rank * 16 + m) * 128] = __uint_as_float(v[m]);
         }
-        uint32_t out[8];
+        uint16_t *y = args.p.y + (int64_t)m0 * N + n;
+        constexpr int kRows = NT == 16 ? 4 : 16;  // at a time
+#pragma unroll 1
+        for (int m = 0; m < rows; m += kRows) {
+          float t[kRows];
 #pragma unroll
-        for (int m = 0; m < 16; m += 2) {
-          t[m] = __fadd_rn(t[m], bv);
-          t[m + 1] = __fadd_rn(t[m + 1], bv);
-          if (m0 + m < M) apply_act_pair(t[m], t[m + 1], args.p.act);
-          out[m / 2] = n < N ? pack_bf16x2(t[m], t[m + 1]) : 0u;
-        }
-        if (!args.p.y_image) {
-          if (n < N) {
-            uint16_t *y = args.p.y + (int64_t)m0 * N + n;
+          for (int j = 0; j < kRows; ++j) t[j] = 0.0f;
+          // the parts in rank order (rows past the last one are not used)
+          for (int r = 0; r < C; ++r)
 #pragma unroll
-            for (int m = 0; m < 16; ++m)
-              if (m0 + m < M) y[(int64_t)m * N] = (uint16_t)((m & 1) ? out[m / 2] >> 16 : out[m / 2] & 0xFFFFu);
+            for (int j = 0; j < kRows; ++j) t[j] += part[(r * 16 + m + j) * 128];
+#pragma unroll
+          for (int j = 0; j < kRows; ++j) t[j] = __fadd_rn(t[j], bv);
+          if (args.p.act != W8A8_ACT_NONE) {
+#pragma unroll
+            for (int j = 0; j < kRows; j += 2) apply_act_pair(t[j], t[j + 1], args.p.act);
           }
-        } else {
-          // a block is the warp's 32 columns of one row of y
-          uint8_t *tile = args.p.y_image + (size_t)(nb >> 1) * kMxTileBytes;
-          const int blk = (nb & 1) * 4 + quarter;
-          const bool pad = !(nb & 1) && (nb + 1) * 128 >= N;  // the tile's other half has no slab
 #pragma unroll
-          for (int m = 0; m < 16; ++m) {
-            const int row = m0 + m;
-            if (row >= M) break;  // uniform
-            const uint32_t bits = (m & 1) ? out[m / 2] >> 16 : out[m / 2] & 0xFFFFu;
-            const uint32_t code = mx4_scale_code(__reduce_max_sync(0xFFFFFFFFu, bits & 0x7FFFu));
-            uint32_t word = mx4_code1(__uint_as_float(bits << 16), code) << (4 * (lane & 7));
-            word |= __shfl_xor_sync(0xFFFFFFFFu, word, 1);
-            word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2);
-            word |= __shfl_xor_sync(0xFFFFFFFFu, word, 4);
-            if ((lane & 7) == 0) {
-              *reinterpret_cast<uint32_t *>(tile + mx4_chunk_offset(row, blk) + (lane >> 3) * 4) = word;
-              if (pad)
-                *reinterpret_cast<uint32_t *>(tile + mx4_chunk_offset(row, blk + 4) + (lane >> 3) * 4) = 0u;
-            }
-            if (lane == 0) {
-              tile[mx4_scale_offset(row, blk)] = (uint8_t)code;
-              if (pad) tile[mx4_scale_offset(row, blk + 4)] = 0;
+          for (int j = 0; j < kRows; j += 2) {
+            const uint32_t out = n < N ? pack_bf16x2(t[j], t[j + 1]) : 0u;
+            const bool one = m + j < rows, two = m + j + 1 < rows;
+            if (args.p.y_image) {
+              if (one) image_row(args.p, m0 + m + j, nb, quarter, lane, out & 0xFFFFu);
+              if (two) image_row(args.p, m0 + m + j + 1, nb, quarter, lane, out >> 16);
+            } else if (n < N) {
+              if (one) y[(m + j) * (int64_t)N] = (uint16_t)out;
+              if (two) y[(m + j + 1) * (int64_t)N] = (uint16_t)(out >> 16);
             }
           }
         }
