@@ -378,9 +378,11 @@ w8a8_status w8a8_mx4_linear_quant(const void *x, int64_t ldx, const void *w_imag
  * g is the row's group (image, sequence): group_index[m], or m /
  * rows_per_group.  A row whose group_index is outside [0, groups) is padding:
  * it is not computed and its outputs keep what they held.
- * Limits: K % 8 == 0 (K % 16 == 0 with q or image), K <= 32768, strides in
- * elements and multiples of 16 bytes, all pointers 16-byte aligned
- * (group_index 4).  residual_out may be residual (with the same stride);
+ * Limits: K % 8 == 0 (K % 16 == 0 with q or image), K <= 16384 (14336 where
+ * post.bias, one of gate and post.weight, one of pre.weight and scale, and one
+ * of pre.bias and shift are all given: a group's vectors are kept in shared
+ * memory), strides in elements and multiples of 16 bytes, all pointers
+ * 16-byte aligned (group_index 4).  residual_out may be residual (with the same stride);
  * otherwise outputs do not overlap inputs. */
 typedef enum { W8A8_NORM_NONE = 0, W8A8_NORM_RMS = 1, W8A8_NORM_LAYER = 2 } w8a8_norm_kind;
 typedef enum { W8A8_DTYPE_BF16 = 0, W8A8_DTYPE_FP32 = 1 } w8a8_dtype;

@@ -84,7 +84,7 @@ def tensors(seed, M, K, groups=0, dtype=torch.bfloat16, mean=0.0):
     return x, r, (n(K, std=0.2, m=1.0), n(K, std=0.2)), (n(K, std=0.2, m=1.0), n(K, std=0.2)), mod
 
 
-SHAPES = [(1, 8), (1, 5120), (3, 24), (5, 264), (7, 1000), (130, 2048), (33, 4104), (4, 12288), (2, 16392), (2, 32768)]
+SHAPES = [(1, 8), (1, 5120), (3, 24), (5, 264), (7, 1000), (130, 2048), (33, 4104), (4, 12288), (2, 14336), (5, 10008)]
 
 
 @pytest.mark.parametrize("M,K", SHAPES)
@@ -113,7 +113,7 @@ def test_norms_around_the_residual(M, K, kind, dtype):
         assert (out.y is None) == ("pre" not in kw)
 
 
-@pytest.mark.parametrize("M,K", [(1, 16), (1, 5120), (5, 272), (129, 1040), (300, 2048), (3, 12288), (2, 32768)])
+@pytest.mark.parametrize("M,K", [(1, 16), (1, 5120), (5, 272), (129, 1040), (300, 2048), (3, 12288), (2, 14336), (1200, 64)])
 @pytest.mark.parametrize("codes", ["int8", "mx4"])
 def test_codes_are_those_of_the_output(M, K, codes):
     x, r, (pw, _), (w, b), (gate, scale, shift) = tensors(M + 5 * K, M, K, 1)
@@ -172,6 +172,26 @@ def test_group_index_and_padding_rows():
     c, s = out.mx4.unpack()
     cw, sw = w8.mx4_quant(out.y).unpack()
     assert torch.equal(c[keep], cw[keep]) and torch.equal(s[keep], sw[keep])
+
+
+@pytest.mark.parametrize("M,K", [(1500, 264), (700, 1040), (400, 4104)])
+def test_many_rows_with_a_group_and_padding_each(M, K):
+    """Several rows a CTA, groups that change and recur, padding rows between them, one norm or both."""
+    groups = 7
+    x, r, (pw, pb), (w, b), (gate, scale, shift) = tensors(M, M, K, groups)
+    index = torch.randint(-1, groups + 1, (M,), dtype=torch.int32, device="cuda")
+    index[100:200] = 3
+    index[-40:] = -1
+    keep = ((index >= 0) & (index < groups)).nonzero().flatten()
+    for kw in (dict(post=w8.Norm("layer", pw, pb), gate=gate, pre=w8.Norm("rms", w), scale=scale, shift=shift),
+               dict(pre=w8.Norm("layer", w, b), scale=scale), dict(gate=gate), dict(post=w8.Norm("rms"), gate=gate)):
+        stream = torch.full_like(r, 7.0)
+        out = w8.block_norm(x, r, residual_out=stream, group_index=index, **kw)
+        some = type(out)(*(t[keep] if torch.is_tensor(t) else t for t in out))
+        check(some, x[keep], r[keep], kw, index[keep].cpu().numpy())
+        skipped = torch.ones(M, dtype=torch.bool, device="cuda")
+        skipped[keep] = False
+        assert (stream[skipped] == 7.0).all()
 
 
 def test_strides_and_leading_sizes():

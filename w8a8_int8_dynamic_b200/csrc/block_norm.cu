@@ -10,13 +10,23 @@
 //   layer(t) = (t - mean) * rsqrt(mean((t - mean)^2) + eps) * w + b
 //   y = bf16(h);  int8 codes and row scale of y;  MX 4-bit image of y
 //
-// A row belongs to W warps, each lane holding CPL chunks of eight elements:
-// x and the residual are read once, at the start, and everything until the
-// stores stays in registers in fp32.  The mean is taken before the squares of
-// the differences (no cancellation, whatever the mean).  The modulation and
-// weight vectors are shared by many rows and come through L1.  Memory-bound:
-// (2 + r) bytes read and (r + 2 | 1 | 17/32) written an element, r the bytes of
-// the residual's type.
+// A CTA of W warps takes a run of rows, each lane holding CPL chunks of eight
+// elements: x and the residual are read once and everything until the stores
+// stays in registers in fp32.  The loads of the next row are in flight while
+// the CTA works on this one.
+//
+// What is shared by a group's rows is folded once per run of rows of a group,
+// into fp32 vectors in shared memory: gate * post weight, pre weight * (1 +
+// scale), pre bias * (1 + scale) + shift.  A row then costs two or three
+// multiply-adds an element for them; widening up to seven bf16 vectors again
+// for every row made the kernel instruction-bound (52 instructions an element,
+// 8192 x 4096: 76 us).  The arithmetic runs on paired fp32 instructions.
+// Memory-bound: (2 + r) bytes read and (r + 2 | 1 | 17/32) written an element,
+// r the bytes of the residual's type.
+//
+// The mean and the sum of squared differences of a row take one barrier: each
+// warp forms both of its own part (the mean first, so nothing cancels), and
+// the parts are joined as sum(m2) + sum(n (mean - total mean)^2).
 //
 // A programmatic dependent that releases the next kernel at its start and
 // touches memory only after its own wait.
@@ -45,239 +55,466 @@ struct NormArgs {
   int post_kind, pre_kind;
   int residual_f32;
   float residual_scale, post_eps, pre_eps, inv_k;
-  int W, R;  // warps per row, rows per CTA
+  int W;        // warps per row
+  int folded;   // which folded vectors there are (kFold*)
+  int padded;   // chunks of a folded vector: W * 32 * chunks per lane
 };
 
-__device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]) {
-  f[0] = bf16_lo(v.x), f[1] = bf16_hi(v.x), f[2] = bf16_lo(v.y), f[3] = bf16_hi(v.y);
-  f[4] = bf16_lo(v.z), f[5] = bf16_hi(v.z), f[6] = bf16_lo(v.w), f[7] = bf16_hi(v.w);
-}
+// Eight values as four fp32 pairs.
+struct Eight {
+  uint64_t p[4];
+};
 
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+__device__ __forceinline__ uint64_t widen(uint32_t w) {
+  return f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ Eight widen8(const uint4 &v) {
+  return {{widen(v.x), widen(v.y), widen(v.z), widen(v.w)}};
+}
+__device__ __forceinline__ uint32_t narrow(uint64_t p) {
+  float lo, hi;
+  f2_unpack(p, lo, hi);
   const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&r);
 }
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+__device__ __forceinline__ uint4 narrow8(const Eight &e) {
+  return make_uint4(narrow(e.p[0]), narrow(e.p[1]), narrow(e.p[2]), narrow(e.p[3]));
+}
+__device__ __forceinline__ float pair_sum(uint64_t p) {
+  float lo, hi;
+  f2_unpack(p, lo, hi);
+  return lo + hi;
 }
 
-// Eight parameters of a vector (bf16), through L1; `fill` where there is none.
-__device__ __forceinline__ void params8(const uint16_t *p, int c, float fill, float (&f)[8]) {
-  if (p) {
-    unpack8(__ldg(reinterpret_cast<const uint4 *>(p) + c), f);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = fill;
-  }
-}
-
-constexpr int kMaxWarps = 16;
-
-// Sum over the row's W warps, the same in every lane.  Each call of a row has
-// a shared-memory line of its own (`line`), so one barrier a call is enough.
-__device__ __forceinline__ float row_sum(float v, float (*lines)[kMaxWarps], int line, int rl, int w,
-                                         int W, int lane) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  if (W > 1) {
-    float *l = lines[line] + rl * W;
-    if (lane == 0) l[w] = v;
-    __syncthreads();
-    v = 0.0f;
-    for (int i = 0; i < W; ++i) v += l[i];
-  }
+// 16 bytes that are read once; not through the read-only path, since the
+// residual may be updated in place.
+__device__ __forceinline__ uint4 ld_once(const void *p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
   return v;
 }
 
-// Normalises the lane's chunks of a row in place (without modulation).
+constexpr int kMaxWarps = 16;  // of a row: lanes 0..15 join their parts
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+// Sum over lanes 0..15 (in every one of them and, of zeros, above), the same everywhere.
+__device__ __forceinline__ float half_sum(float v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return __shfl_sync(0xFFFFFFFFu, v, 0);
+}
+
+// Where a warp stands: its part of the row.
+struct Place {
+  int w, W, lane, c0, nchunks;
+  float own_count;   // elements of the row in this warp's part
+  float lane_count;  // elements in the part of warp `lane` (0: no such warp)
+};
+
+// A row's norm as t -> t * rstd + offset, for t with this warp's mean taken off.
+struct Stat {
+  uint64_t rstd, offset;
+};
+
+// Takes the mean of the warp's part off t and joins the warps' parts.  `line`:
+// shared memory of this call and row parity, so one barrier a call is enough.
 template <int CPL>
-__device__ __forceinline__ void normalise(float (&t)[CPL][8], int kind, float eps, float inv_k,
-                                          const uint16_t *wp, const uint16_t *bp, int c0, int nchunks,
-                                          float (*lines)[kMaxWarps], int line, int rl, int w, int W,
-                                          int lane) {
-  float mean = 0.0f;
-  if (kind == W8A8_NORM_LAYER) {
-    float s = 0.0f;
+__device__ __forceinline__ Stat centre(Eight (&t)[CPL], int kind, float eps, float inv_k, float2 *line,
+                                       const Place &at) {
+  float own = 0.0f;
+  const bool layer = kind == W8A8_NORM_LAYER;
+  if (layer) {
+    uint64_t s[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < CPL; ++j)
+      if (at.c0 + 32 * j < at.nchunks) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] = f2_add(s[i], t[j].p[i]);
+      }
+    const float sum = warp_sum(pair_sum(f2_add(f2_add(s[0], s[1]), f2_add(s[2], s[3]))));
+    own = at.own_count > 0.0f ? __fdividef(sum, at.own_count) : 0.0f;
+    const uint64_t neg = f2_splat(-own);
 #pragma unroll
     for (int j = 0; j < CPL; ++j)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s += t[j][i];
-    mean = row_sum(s, lines, line, rl, w, W, lane) * inv_k;
+      for (int i = 0; i < 4; ++i) t[j].p[i] = f2_add(t[j].p[i], neg);
   }
-  float s = 0.0f;
+  uint64_t q[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int j = 0; j < CPL; ++j)
-    if (c0 + 32 * j < nchunks) {  // chunks past the row hold zeros, whose difference is not zero
+    if (at.c0 + 32 * j < at.nchunks) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        t[j][i] -= mean;
-        s = __fmaf_rn(t[j][i], t[j][i], s);
-      }
+      for (int i = 0; i < 4; ++i) q[i] = f2_fma(t[j].p[i], t[j].p[i], q[i]);
     }
-  const float rstd = rsqrtf(row_sum(s, lines, line + 1, rl, w, W, lane) * inv_k + eps);
+  float m2 = warp_sum(pair_sum(f2_add(f2_add(q[0], q[1]), f2_add(q[2], q[3])))), offset = 0.0f;
+  if (at.W > 1) {
+    if (at.lane == 0) line[at.w] = make_float2(own, m2);
+    __syncthreads();
+    float2 part = make_float2(0.0f, 0.0f);
+    if (at.lane < at.W) part = line[at.lane];
+    if (layer) {
+      const float mean = half_sum(part.x * at.lane_count) * inv_k;
+      const float d = part.x - mean;
+      part.y = __fmaf_rn(d * d, at.lane_count, part.y);
+      offset = own - mean;
+    }
+    m2 = half_sum(part.y);
+  }
+  const float rstd = rsqrtf(__fmaf_rn(m2, inv_k, eps));
+  return {f2_splat(rstd), f2_splat(offset * rstd)};
+}
+
+// Folded vectors in shared memory, present or not.  A vector is stored by 32
+// chunks at a time: the first four values of each of the 32, then the last
+// four, so that a warp's 16-byte reads are consecutive and all of a lane's are
+// at constant offsets from one address.  It is as long as the warps' parts
+// (a.padded chunks); what is past the row is never written and never used.
+enum { kFoldBranch = 1, kFoldBranchAdd = 2, kFoldMul = 4, kFoldAdd = 8 };
+
+// `v`: this lane's address in the vector, for its chunk j.
+__device__ __forceinline__ Eight load_fold(const ulonglong2 *v, int j) {
+  const ulonglong2 lo = v[j * 64], hi = v[j * 64 + 32];
+  return {{lo.x, lo.y, hi.x, hi.y}};
+}
+__device__ __forceinline__ void store_fold(ulonglong2 *v, int c, const Eight &e) {
+  v += (c >> 5) * 64 + (c & 31);
+  v[0] = make_ulonglong2(e.p[0], e.p[1]);
+  v[32] = make_ulonglong2(e.p[2], e.p[3]);
+}
+
+// Folds the vectors of group g (all threads of the CTA; the caller syncs).
+// Every load of a thread's chunks before the first use: one after another they
+// took 20 us of an 8192 x 4096 launch.
+__device__ __forceinline__ void fold(const NormArgs &a, ulonglong2 *v, int64_t g) {
+  const int nchunks = a.K >> 3;
+  const uint64_t one = f2_splat(1.0f);
+  constexpr int kAtOnce = 1;
+  auto get = [](const uint16_t *p, int c, uint4 &d) {
+    if (p) d = __ldg(reinterpret_cast<const uint4 *>(p) + c);
+  };
+  const uint16_t *gp = a.gate ? a.gate + g * a.ld_gate : nullptr;
+  const uint16_t *sp = a.scale ? a.scale + g * a.ld_scale : nullptr;
+  const uint16_t *tp = a.shift ? a.shift + g * a.ld_shift : nullptr;
+  for (int c0 = threadIdx.x; c0 < nchunks; c0 += kAtOnce * blockDim.x) {
+    uint4 gate[kAtOnce], pw[kAtOnce], pb[kAtOnce], sc[kAtOnce], w[kAtOnce], b[kAtOnce], sh[kAtOnce];
 #pragma unroll
-  for (int j = 0; j < CPL; ++j) {
-    const int c = c0 + 32 * j;
-    if (c < nchunks) {
-      float wv[8], bv[8];
-      params8(wp, c, 1.0f, wv);
-      params8(bp, c, 0.0f, bv);
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int c = min(c0 + k * (int)blockDim.x, nchunks - 1);
+      get(gp, c, gate[k]);
+      get(a.post_w, c, pw[k]);
+      get(a.post_b, c, pb[k]);
+      get(sp, c, sc[k]);
+      get(a.pre_w, c, w[k]);
+      get(a.pre_b, c, b[k]);
+      get(tp, c, sh[k]);
+    }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) t[j][i] = __fmaf_rn(t[j][i] * rstd, wv[i], bv[i]);
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int c = c0 + k * (int)blockDim.x;
+      if (c >= nchunks) break;
+      ulonglong2 *to = v;
+      auto emit = [&](const Eight &e) {
+        store_fold(to, c, e);
+        to += a.padded * 2;
+      };
+      Eight e{{one, one, one, one}};
+      if (gp) e = widen8(gate[k]);
+      Eight f = e;
+      if (a.post_w) {
+        const Eight m = widen8(pw[k]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f.p[i] = f2_mul(f.p[i], m.p[i]);
+      }
+      if (a.folded & kFoldBranch) emit(f);
+      if (a.folded & kFoldBranchAdd) {
+        f = widen8(pb[k]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f.p[i] = f2_mul(f.p[i], e.p[i]);
+        emit(f);
+      }
+      e = {{one, one, one, one}};
+      if (sp) {
+        e = widen8(sc[k]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e.p[i] = f2_add(e.p[i], one);
+      }
+      f = e;
+      if (a.pre_w) {
+        const Eight m = widen8(w[k]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f.p[i] = f2_mul(f.p[i], m.p[i]);
+      }
+      if (a.folded & kFoldMul) emit(f);
+      if (a.folded & kFoldAdd) {
+        f = {{0, 0, 0, 0}};
+        if (tp) f = widen8(sh[k]);
+        if (a.pre_b) {
+          const Eight m = widen8(b[k]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f.p[i] = f2_fma(m.p[i], e.p[i], f.p[i]);
+        }
+        emit(f);
+      }
     }
   }
 }
 
-template <int CPL>
-__global__ void __launch_bounds__(512) block_norm_kernel(const NormArgs a) {
-  __shared__ float lines[5][kMaxWarps];
+enum { kNoResidual = 0, kResidualBf16 = 1, kResidualF32 = 2 };
+
+// A row as it was loaded.
+template <int CPL, int RES>
+struct Raw {
+  uint4 x[CPL];
+  uint4 r0[RES == kNoResidual ? 1 : CPL], r1[RES == kResidualF32 ? CPL : 1];
+};
+
+// x, r: this lane's first chunk of the row (elements past the row read as zeros).
+template <int CPL, int RES>
+__device__ __forceinline__ void fetch(const uint8_t *x, const uint8_t *r, const Place &at, Raw<CPL, RES> &d) {
+#pragma unroll
+  for (int j = 0; j < CPL; ++j) {
+    const bool in = at.c0 + 32 * j < at.nchunks;
+    d.x[j] = make_uint4(0, 0, 0, 0);
+    if (in) d.x[j] = ld_once(x + j * 512);
+    if constexpr (RES == kResidualF32) {
+      d.r0[j] = d.r1[j] = make_uint4(0, 0, 0, 0);
+      if (in) {
+        d.r0[j] = ld_once(r + j * 1024);
+        d.r1[j] = ld_once(r + j * 1024 + 16);
+      }
+    } else if constexpr (RES == kResidualBf16) {
+      d.r0[j] = make_uint4(0, 0, 0, 0);
+      if (in) d.r0[j] = ld_once(r + j * 512);
+    }
+  }
+}
+
+template <int CPL, int RES, int REGS>
+__global__ void __maxnreg__(REGS) block_norm_kernel(const __grid_constant__ NormArgs a) {
+  extern __shared__ ulonglong2 folded[];
+  __shared__ float2 lines[2][2][kMaxWarps];     // [row parity][norm][warp]
+  __shared__ uint32_t max_lines[2][kMaxWarps];  // [row parity][warp]
   griddep_launch_dependents();
   griddep_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int W = a.W, rl = warp / W, w = warp - rl * W;
-  const int64_t row = (int64_t)blockIdx.x * a.R + rl;
-  const int nchunks = a.K >> 3;
-  const int c0 = w * 32 * CPL + lane;
-  bool active = row < a.M;
-  int64_t g = 0;
-  if (active) {
+  Place at;
+  at.lane = threadIdx.x & 31;
+  at.w = threadIdx.x >> 5;
+  at.W = a.W;
+  at.nchunks = a.K >> 3;
+  at.c0 = at.w * 32 * CPL + at.lane;
+  auto count = [&](int w) { return (float)(max(0, min(at.nchunks - w * 32 * CPL, 32 * CPL)) * 8); };
+  at.own_count = count(at.w);
+  at.lane_count = at.lane < at.W ? count(at.lane) : 0.0f;
+  // this lane's place in a folded vector, of which `before` are stored ahead
+  auto place = [&](int before) {
+    return folded + (at.w * 64 * CPL + at.lane) + __popc(a.folded & before) * a.padded * 2;
+  };
+
+  constexpr int kRes = RES == kResidualF32 ? 4 : 2;  // bytes of the residual's type
+  int have = -1;   // the group whose vectors are folded
+  int parity = 0;  // of the rows computed: each leaves the other its barrier lines
+  int row = (int)((int64_t)a.M * blockIdx.x / gridDim.x);
+  const int end = (int)((int64_t)a.M * (blockIdx.x + 1) / gridDim.x);
+  while (row < end) {
+    // a run of rows of one group
+    int group = 0, run = end;
     if (a.group_index) {
-      g = a.group_index[row];
-      active = g >= 0 && g < a.groups;  // a padding row: its outputs keep what they hold
+      group = a.group_index[row];
+      for (run = row + 1; run < end && a.group_index[run] == group;) ++run;
+      if (group < 0 || group >= a.groups) {  // padding rows: their outputs keep what they hold
+        row = run;
+        continue;
+      }
     } else if (a.rows_per_group) {
-      g = row / a.rows_per_group;
+      group = (int)(row / a.rows_per_group);
+      run = (int)min((int64_t)end, (group + 1) * a.rows_per_group);
     }
-  }
-
-  // every load of the row first, so that they are in flight together
-  uint4 xr[CPL], r0[CPL], r1[CPL];
-#pragma unroll
-  for (int j = 0; j < CPL; ++j) {
-    const int c = c0 + 32 * j;
-    const bool in = active && c < nchunks;
-    xr[j] = r0[j] = r1[j] = make_uint4(0, 0, 0, 0);
-    if (in) xr[j] = ld_stream_u4(a.x + row * a.ldx + (int64_t)c * 8);
-    if (in && a.residual) {
-      if (a.residual_f32) {
-        const float *p = static_cast<const float *>(a.residual) + row * a.ldr + (int64_t)c * 8;
-        r0[j] = *reinterpret_cast<const uint4 *>(p);
-        r1[j] = *reinterpret_cast<const uint4 *>(p + 4);
-      } else {
-        r0[j] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.residual) +
-                                                 row * a.ldr + (int64_t)c * 8);
-      }
-    }
-  }
-  float t[CPL][8];
-#pragma unroll
-  for (int j = 0; j < CPL; ++j) unpack8(xr[j], t[j]);
-
-  if (a.post_kind != W8A8_NORM_NONE)
-    normalise<CPL>(t, a.post_kind, a.post_eps, a.inv_k, a.post_w, a.post_b, c0, nchunks, lines, 0, rl, w,
-                   W, lane);
-
-  if (a.residual) {
-    const uint16_t *gate = a.gate ? a.gate + g * a.ld_gate : nullptr;
-#pragma unroll
-    for (int j = 0; j < CPL; ++j) {
-      const int c = c0 + 32 * j;
-      if (!(active && c < nchunks)) continue;
-      float r[8], gv[8];
-      if (a.residual_f32) {
-        const uint32_t b[8] = {r0[j].x, r0[j].y, r0[j].z, r0[j].w, r1[j].x, r1[j].y, r1[j].z, r1[j].w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) r[i] = __uint_as_float(b[i]);
-      } else {
-        unpack8(r0[j], r);
-      }
-      params8(gate, c, 1.0f, gv);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) t[j][i] = __fmaf_rn(gv[i], t[j][i], a.residual_scale * r[i]);
-      if (a.residual_f32) {
-        float *p = static_cast<float *>(a.residual_out) + row * a.ldro + (int64_t)c * 8;
-        *reinterpret_cast<float4 *>(p) = make_float4(t[j][0], t[j][1], t[j][2], t[j][3]);
-        *reinterpret_cast<float4 *>(p + 4) = make_float4(t[j][4], t[j][5], t[j][6], t[j][7]);
-      } else {
-        const uint4 v = pack8(t[j]);
-        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.residual_out) + row * a.ldro +
-                                   (int64_t)c * 8) = v;
-        unpack8(v, t[j]);  // the norm is of the stream as it is stored
-      }
-    }
-  }
-
-  if (a.pre_kind == W8A8_NORM_NONE) return;
-  normalise<CPL>(t, a.pre_kind, a.pre_eps, a.inv_k, a.pre_w, a.pre_b, c0, nchunks, lines, 2, rl, w, W,
-                 lane);
-
-  const uint16_t *scale = a.scale ? a.scale + g * a.ld_scale : nullptr;
-  const uint16_t *shift = a.shift ? a.shift + g * a.ld_shift : nullptr;
-  uint4 h[CPL];
-  uint32_t mx = 0;
-#pragma unroll
-  for (int j = 0; j < CPL; ++j) {
-    const int c = c0 + 32 * j;
-    h[j] = make_uint4(0, 0, 0, 0);
-    if (!(active && c < nchunks)) continue;
-    if (scale || shift) {
-      float sv[8], tv[8];
-      params8(scale, c, 0.0f, sv);
-      params8(shift, c, 0.0f, tv);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) t[j][i] = __fmaf_rn(t[j][i], 1.0f + sv[i], tv[i]);
-    }
-    h[j] = pack8(t[j]);
-    if (a.y) *reinterpret_cast<uint4 *>(a.y + row * a.ldy + (int64_t)c * 8) = h[j];
-    mx = absmax_chunk(mx, h[j]);
-  }
-
-  if (a.q) {  // as the int8 quantisation kernel, on the rounded row
-    uint32_t m = absmax_fold(mx);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    if (W > 1) {
-      uint32_t *l = reinterpret_cast<uint32_t *>(lines[4]) + rl * W;
-      if (lane == 0) l[w] = m;
+    if (a.folded && group != have) {
       __syncthreads();
-      for (int i = 0; i < W; ++i) m = max(m, l[i]);
+      fold(a, folded, group);
+      __syncthreads();
+      have = group;
     }
-    if (active) {
-      const float amax = __uint_as_float(m << 16);
-      const float s = amax == 0.0f ? 0.0f : __fdiv_rn(amax, 127.0f);
-      const float inv = amax == 0.0f ? 0.0f : __frcp_rn(s);
-      if (w == 0 && lane == 0) a.a_scale[row] = s;
+    auto load = [&](int i, Raw<CPL, RES> &d) {
+      fetch<CPL, RES>(reinterpret_cast<const uint8_t *>(a.x + i * a.ldx + at.c0 * 8),
+                      static_cast<const uint8_t *>(a.residual) + (i * a.ldr + at.c0 * 8) * kRes, at, d);
+    };
+    Raw<CPL, RES> next;
+    load(row, next);
+    for (; row < run; ++row) {
+      const Raw<CPL, RES> cur = next;
+      if (row + 1 < run) load(row + 1, next);
+      parity ^= 1;
+      Eight t[CPL];
+#pragma unroll
+      for (int j = 0; j < CPL; ++j) t[j] = widen8(cur.x[j]);
+
+      if constexpr (RES != kNoResidual) {
+        uint8_t *ro = static_cast<uint8_t *>(a.residual_out) + (row * a.ldro + at.c0 * 8) * kRes;
+        const bool post = a.post_kind != W8A8_NORM_NONE;
+        Stat st = {};
+        if (post) st = centre<CPL>(t, a.post_kind, a.post_eps, a.inv_k, lines[parity][0], at);
+        const uint64_t rs = f2_splat(a.residual_scale);
+        // (No branch on a chunk past the row: it computes on what it finds and is
+        // not stored, so that the chunks' reads of shared memory can be in flight
+        // together.)
+#pragma unroll
+        for (int j = 0; j < CPL; ++j) {
+          const bool in = at.c0 + 32 * j < at.nchunks;
+          if (post) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t[j].p[i] = f2_fma(t[j].p[i], st.rstd, st.offset);
+          }
+          Eight r;
+          if constexpr (RES == kResidualF32) {
+            r.p[0] = f2_pack(__uint_as_float(cur.r0[j].x), __uint_as_float(cur.r0[j].y));
+            r.p[1] = f2_pack(__uint_as_float(cur.r0[j].z), __uint_as_float(cur.r0[j].w));
+            r.p[2] = f2_pack(__uint_as_float(cur.r1[j].x), __uint_as_float(cur.r1[j].y));
+            r.p[3] = f2_pack(__uint_as_float(cur.r1[j].z), __uint_as_float(cur.r1[j].w));
+          } else {
+            r = widen8(cur.r0[j]);
+          }
+          if (a.folded & kFoldBranchAdd) {
+            const Eight e = load_fold(place(kFoldBranch), j);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r.p[i] = f2_fma(r.p[i], rs, e.p[i]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r.p[i] = f2_mul(r.p[i], rs);
+          }
+          if (a.folded & kFoldBranch) {
+            const Eight e = load_fold(place(0), j);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t[j].p[i] = f2_fma(t[j].p[i], e.p[i], r.p[i]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t[j].p[i] = f2_add(t[j].p[i], r.p[i]);
+          }
+          if constexpr (RES == kResidualF32) {
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f2_unpack(t[j].p[i], f[2 * i], f[2 * i + 1]);
+            if (in) {
+              float4 *p = reinterpret_cast<float4 *>(ro + j * 1024);
+              p[0] = make_float4(f[0], f[1], f[2], f[3]);
+              p[1] = make_float4(f[4], f[5], f[6], f[7]);
+            }
+          } else {
+            const uint4 v = narrow8(t[j]);
+            if (in) *reinterpret_cast<uint4 *>(ro + j * 512) = v;
+            t[j] = widen8(v);  // the norm is of the stream as it is stored
+          }
+        }
+        if (a.pre_kind == W8A8_NORM_NONE) continue;
+      }
+
+      const Stat st = centre<CPL>(t, a.pre_kind, a.pre_eps, a.inv_k, lines[parity][1], at);
+      uint16_t *y = a.y + row * a.ldy + at.c0 * 8;
+      uint4 h[CPL];
+      uint32_t mx = 0;
 #pragma unroll
       for (int j = 0; j < CPL; ++j) {
-        const int c = c0 + 32 * j;
-        if (c >= nchunks) continue;
-        uint2 out = make_uint2(0, 0);
-        if (amax != 0.0f) out = s >= 1e-30f ? codes8(h[j], s, inv) : codes8_ieee(h[j], s);
-        *reinterpret_cast<uint2 *>(a.q + row * (int64_t)a.K + (int64_t)c * 8) = out;
-      }
-    }
-  }
-
-  if (a.image && active) {
-    // a block is the four chunks of four neighbouring lanes; the image's
-    // columns past K (to 256) are written too, as zeros
-    const int r = (int)(row & 127);
+        const bool in = at.c0 + 32 * j < at.nchunks;
 #pragma unroll
-    for (int j = 0; j < CPL; ++j) {
-      const int c = c0 + 32 * j;
-      uint32_t m = absmax_chunk(0, h[j]);
-      m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-      m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-      const uint32_t code = mx4_scale_code(mx4_max_bits(m));
-      if (c < a.kt * 32) {
-        uint8_t *tile = a.image + ((size_t)(row >> 7) * a.kt + (c >> 5)) * kMxTileBytes;
-        const int b = (c >> 2) & 7;
-        *reinterpret_cast<uint32_t *>(tile + mx4_chunk_offset(r, b) + (c & 3) * 4) =
-            mx4_encode8(h[j], code);
-        if ((c & 3) == 0) tile[mx4_scale_offset(r, b)] = (uint8_t)code;
+        for (int i = 0; i < 4; ++i) t[j].p[i] = f2_fma(t[j].p[i], st.rstd, st.offset);
+        if (a.folded & kFoldMul) {
+          const Eight m = load_fold(place(kFoldBranch | kFoldBranchAdd), j);
+          if (a.folded & kFoldAdd) {
+            const Eight e = load_fold(place(kFoldBranch | kFoldBranchAdd | kFoldMul), j);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t[j].p[i] = f2_fma(t[j].p[i], m.p[i], e.p[i]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t[j].p[i] = f2_mul(t[j].p[i], m.p[i]);
+          }
+        } else if (a.folded & kFoldAdd) {
+          const Eight e = load_fold(place(kFoldBranch | kFoldBranchAdd | kFoldMul), j);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) t[j].p[i] = f2_add(t[j].p[i], e.p[i]);
+        }
+        h[j] = narrow8(t[j]);
+        if (!in) h[j] = make_uint4(0, 0, 0, 0);
+        if (in && a.y) *reinterpret_cast<uint4 *>(y + j * 256) = h[j];
+        mx = absmax_chunk(mx, h[j]);
+      }
+
+      if (a.q) {  // as the int8 quantisation kernel, on the rounded row
+        uint32_t m = absmax_fold(mx);
+        m = __reduce_max_sync(0xFFFFFFFFu, m);
+        if (at.W > 1) {
+          if (at.lane == 0) max_lines[parity][at.w] = m;
+          __syncthreads();
+          m = at.lane < at.W ? max_lines[parity][at.lane] : 0u;
+          m = __reduce_max_sync(0xFFFFFFFFu, m);
+        }
+        {
+          const float amax = __uint_as_float(m << 16);
+          const float s = amax == 0.0f ? 0.0f : __fdiv_rn(amax, 127.0f);
+          const float inv = amax == 0.0f ? 0.0f : __frcp_rn(s);
+          if (at.w == 0 && at.lane == 0) a.a_scale[row] = s;
+#pragma unroll
+          for (int j = 0; j < CPL; ++j) {
+            const int c = at.c0 + 32 * j;
+            if (c >= at.nchunks) continue;
+            uint2 out = make_uint2(0, 0);
+            if (amax != 0.0f) out = s >= 1e-30f ? codes8(h[j], s, inv) : codes8_ieee(h[j], s);
+            *reinterpret_cast<uint2 *>(a.q + row * (int64_t)a.K + (int64_t)c * 8) = out;
+          }
+        }
+      }
+
+      if (a.image) {
+        // a block is the four chunks of four neighbouring lanes; the image's
+        // columns past K (to 256) are written too, as zeros
+        const int r = (int)(row & 127);
+#pragma unroll
+        for (int j = 0; j < CPL; ++j) {
+          const int c = at.c0 + 32 * j;
+          uint32_t m = absmax_chunk(0, h[j]);
+          m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+          m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+          const uint32_t code = mx4_scale_code(mx4_max_bits(m));
+          if (c < a.kt * 32) {
+            uint8_t *tile = a.image + ((size_t)(row >> 7) * a.kt + (c >> 5)) * kMxTileBytes;
+            const int b = (c >> 2) & 7;
+            *reinterpret_cast<uint32_t *>(tile + mx4_chunk_offset(r, b) + (c & 3) * 4) =
+                mx4_encode8(h[j], code);
+            if ((c & 3) == 0) tile[mx4_scale_offset(r, b)] = (uint8_t)code;
+          }
+        }
       }
     }
   }
 }
+
+FuncAttrOnce g_norm_attr[3][3];            // [shape of the instance][residual]
+constexpr int kMaxFolded = 4 * 4 * 14336;  // shared memory that a launch may ask for: 224 KB
+
+template <int CPL, int RES, int REGS>
+cudaError_t run(const cudaLaunchConfig_t &cfg, const NormArgs &a) {
+  auto k = block_norm_kernel<CPL, RES, REGS>;
+  if (cfg.dynamicSmemBytes > 40000) {
+    const cudaError_t e = g_norm_attr[CPL == 2 ? 0 : REGS == 128 ? 1 : 2][RES].ensure(
+        [&] { return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxFolded); });
+    if (e != cudaSuccess) return e;
+  }
+  return cudaLaunchKernelEx(&cfg, k, a);
+}
+template <int CPL, int REGS>
+cudaError_t run(const cudaLaunchConfig_t &cfg, const NormArgs &a) {
+  if (!a.residual) return run<CPL, kNoResidual, REGS>(cfg, a);
+  return a.residual_f32 ? run<CPL, kResidualF32, REGS>(cfg, a) : run<CPL, kResidualBf16, REGS>(cfg, a);
+}
+
+constexpr int64_t kMaxNormK = 16384;
 
 bool vector_ok(const void *p, int64_t ld, int64_t K, int64_t groups) {
   return !p || ((groups <= 1 || ld == 0 || ld >= K) && ld >= 0);
@@ -317,7 +554,8 @@ extern "C" w8a8_status w8a8_block_norm(const w8a8_block_norm_args *p, w8a8_strea
   if (!vector_ok(p->gate, p->ld_gate, K, p->groups) || !vector_ok(p->scale, p->ld_scale, K, p->groups) ||
       !vector_ok(p->shift, p->ld_shift, K, p->groups))
     return W8A8_ERR_INVALID_ARG;
-  if (K % ((p->q || p->image) ? 16 : 8) != 0 || K > kMaxWarps * 32 * 8 * 8) return W8A8_ERR_UNSUPPORTED_SHAPE;
+  if (mod && p->groups > 0x7FFFFFFF) return W8A8_ERR_INVALID_ARG;
+  if (K % ((p->q || p->image) ? 16 : 8) != 0 || K > kMaxNormK) return W8A8_ERR_UNSUPPORTED_SHAPE;
   const void *ptrs[] = {p->x, p->residual, p->residual_out, p->y, p->q, p->a_scale, p->image, p->gate,
                         p->scale, p->shift, p->post.weight, p->post.bias, p->pre.weight, p->pre.bias};
   for (const void *q : ptrs)
@@ -356,28 +594,45 @@ extern "C" w8a8_status w8a8_block_norm(const w8a8_block_norm_args *p, w8a8_strea
   a.post_eps = p->post.eps, a.pre_eps = p->pre.eps;
   a.inv_k = 1.0f / (float)K;
 
-  // Chunks per lane: 4, or 8 where a row would need more than 16 warps; an
-  // image's padding columns count (the lanes that hold them write them).
+  a.folded = ((a.gate || a.post_w) ? kFoldBranch : 0) | (a.post_b ? kFoldBranchAdd : 0) |
+             ((a.pre_w || a.scale) ? kFoldMul : 0) | ((a.pre_b || a.shift) ? kFoldAdd : 0);
+  // Chunks per lane.  Two (128 registers): what a warp spends on a row apart
+  // from its elements is then as much as on them, but a row is soon done.
+  // Four (160 registers) for many rows a CTA with a bf16 residual: 8192 x 4096
+  // with both norms 59 us, with two chunks 68; but 2048 x 4096 26 and 23, and
+  // with an fp32 residual 79 and 75.  Four (128 registers) where two would
+  // need more than 16 warps.  An image's padding columns count (the lanes that
+  // hold them write them).
   const int64_t nchunks = a.image ? (int64_t)a.kt * 32 : K / 8;
-  const int64_t per_lane = (nchunks + 31) / 32;
-  int cpl = 1;
-  while (cpl < 4 && cpl < per_lane) cpl *= 2;
-  if ((nchunks + 32 * cpl - 1) / (32 * cpl) > kMaxWarps) cpl = 8;
-  a.W = (int)((nchunks + 32 * cpl - 1) / (32 * cpl));
-  a.R = a.W >= 4 ? 1 : 4 / a.W;  // about 128 threads a CTA
+  int cpl = 2, regs = 128;
+  int64_t resident = 0, smem = 0;
+  auto shape = [&](int c, int r) {
+    cpl = c;
+    regs = r;
+    a.W = (int)((nchunks + 32 * c - 1) / (32 * c));
+    a.padded = a.W * 32 * c;
+    smem = (int64_t)a.padded * 32 * __builtin_popcount((unsigned)a.folded);
+    // CTAs that the device holds, as registers and shared memory allow
+    const int64_t fit = std::min<int64_t>(65536 / r / (32 * a.W), (int64_t)226 * 1024 / (smem + 2048));
+    resident = sm_count() * std::min<int64_t>(32, std::max<int64_t>(1, fit));
+  };
+  shape(4, 160);
+  if (nchunks > kMaxWarps * 64)
+    shape(4, 128);
+  else if (a.residual_f32 || M < 8 * resident)
+    shape(2, 128);
+  if (smem > kMaxFolded) return W8A8_ERR_UNSUPPORTED_SHAPE;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((M + a.R - 1) / a.R));
-  cfg.blockDim = dim3((unsigned)(32 * a.W * a.R));
+  cfg.gridDim = dim3((unsigned)std::min(M, resident));
+  cfg.blockDim = dim3((unsigned)(32 * a.W));
+  cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cpl == 1   ? cudaLaunchKernelEx(&cfg, block_norm_kernel<1>, a)
-                        : cpl == 2 ? cudaLaunchKernelEx(&cfg, block_norm_kernel<2>, a)
-                        : cpl == 4 ? cudaLaunchKernelEx(&cfg, block_norm_kernel<4>, a)
-                                   : cudaLaunchKernelEx(&cfg, block_norm_kernel<8>, a);
+  const cudaError_t e = cpl == 2 ? run<2, 128>(cfg, a) : regs == 128 ? run<4, 128>(cfg, a) : run<4, 160>(cfg, a);
   if (e == cudaSuccess) count_launch();
   return from_cuda(e);
 }
