@@ -7,6 +7,7 @@ rows returns an empty result without a launch.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import math
@@ -28,17 +29,29 @@ def _device(first: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
     return index
 
 
-def _call(index: int, stream, f):
-    """f(raw stream) with the device ``index`` current, on ``stream`` or its current stream."""
-    if stream is None and index == torch.cuda.current_device():  # the common case, without the guards' cost
-        return f(torch._C._cuda_getCurrentRawStream(index))
+def _elsewhere(index: int, stream) -> bool:
+    """Whether a call goes to another device than the current one or to a stream of its own."""
+    return stream is not None or index != torch.cuda.current_device()
+
+
+@contextlib.contextmanager
+def _there(index: int, stream):
+    """That device and stream made current: what the call allocates is that stream's."""
     with torch.cuda.device(index):
         if stream is None:
-            return f(torch._C._cuda_getCurrentRawStream(index))
+            yield
+            return
         if stream.device.index != index:
             raise ValueError(f"stream of {stream.device}, tensors on cuda:{index}")
-        with torch.cuda.stream(stream):  # what the call allocates is this stream's
-            return f(stream.cuda_stream)
+        with torch.cuda.stream(stream):
+            yield
+
+
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _bytes(n: int, index: int) -> torch.Tensor:
+    return torch.empty_strided((n,), (1,), dtype=torch.uint8, device=index)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -96,7 +109,7 @@ def _at(t: Optional[torch.Tensor]) -> Optional[int]:
 
 def _image(image: Optional[torch.Tensor], rows: int, K: int, index: int) -> torch.Tensor:
     if image is None:
-        return torch.empty((mx4_bytes(rows, K) if rows else 0,), dtype=torch.uint8, device=index)
+        return _bytes(mx4_bytes(rows, K) if rows else 0, index)
     _need_cuda(image, "image", torch.uint8)
     if not image.is_contiguous():
         raise ValueError("image must be contiguous")
@@ -106,6 +119,8 @@ def _image(image: Optional[torch.Tensor], rows: int, K: int, index: int) -> torc
 def _output(out: Optional[torch.Tensor], lead: Tuple[int, ...], N: int, index: int) -> torch.Tensor:
     """A new [*lead, N], or ``out`` seen as one."""
     if out is None:
+        if len(lead) == 1:
+            return torch.empty_strided((lead[0], N), (N, 1), dtype=torch.bfloat16, device=index)
         return torch.empty((*lead, N), dtype=torch.bfloat16, device=index)
     _need_cuda(out, "out", torch.bfloat16)
     if not out.is_contiguous():
@@ -115,7 +130,7 @@ def _output(out: Optional[torch.Tensor], lead: Tuple[int, ...], N: int, index: i
 
 def _scratch(workspace: Optional[torch.Tensor], need: int, index: int) -> Tuple[Optional[torch.Tensor], int]:
     if workspace is None:
-        return (torch.empty((need,), dtype=torch.uint8, device=index), need) if need else (None, 0)
+        return (_bytes(need, index), need) if need else (None, 0)
     _need_cuda(workspace, "workspace")
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
@@ -142,15 +157,16 @@ def mx4_quant(x: torch.Tensor, image: Optional[torch.Tensor] = None, stream=None
     """bf16 [..., K] -> its 4-bit image (``image``: a uint8 buffer of ``mx4_bytes`` to write)."""
     _need_cuda(x, "x", torch.bfloat16)
     index, K = _device(x, image), x.shape[-1]
-
-    def f(s):
-        x2, M, ldx = _rows_of(x)
-        out = _image(image, M, K, index)
-        if M:
-            _check(lib().w8a8_mx4_quant(x2.data_ptr(), M, K, ldx, out.data_ptr(), out.numel(), s),
-                   "w8a8_mx4_quant")
-        return MX4Tensor(out, x.shape[:-1], K)
-    return _call(index, stream, f)
+    if _elsewhere(index, stream):
+        with _there(index, stream):
+            return mx4_quant(x, image)
+    s = _raw_stream(index)
+    x2, M, ldx = _rows_of(x)
+    out = _image(image, M, K, index)
+    if M:
+        _check(lib().w8a8_mx4_quant(x2.data_ptr(), M, K, ldx, out.data_ptr(), out.numel(), s),
+               "w8a8_mx4_quant")
+    return MX4Tensor(out, x.shape[:-1], K)
 
 
 def mx4_pack(codes: torch.Tensor, scales: torch.Tensor, image: Optional[torch.Tensor] = None,
@@ -163,43 +179,46 @@ def mx4_pack(codes: torch.Tensor, scales: torch.Tensor, image: Optional[torch.Te
     rows, K = codes.shape[0], codes.shape[1] * 2
     if tuple(scales.shape) != (rows, (K + 31) // 32):
         raise ValueError(f"scales must be [{rows}, {(K + 31) // 32}], got {list(scales.shape)}")
-
-    def f(s):
-        c, e = codes.contiguous(), scales.contiguous()
-        out = _image(image, rows, K, index)
-        if rows:
-            _check(lib().w8a8_mx4_pack(c.data_ptr(), e.data_ptr(), rows, K, out.data_ptr(), out.numel(), s),
-                   "w8a8_mx4_pack")
-        return MX4Tensor(out, (rows,), K)
-    return _call(index, stream, f)
+    if _elsewhere(index, stream):
+        with _there(index, stream):
+            return mx4_pack(codes, scales, image)
+    s = _raw_stream(index)
+    c, e = codes.contiguous(), scales.contiguous()
+    out = _image(image, rows, K, index)
+    if rows:
+        _check(lib().w8a8_mx4_pack(c.data_ptr(), e.data_ptr(), rows, K, out.data_ptr(), out.numel(), s),
+               "w8a8_mx4_pack")
+    return MX4Tensor(out, (rows,), K)
 
 
 def mx4_unpack(t: MX4Tensor, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """image -> (codes [rows, K/2], scales [rows, ceil(K/32)]), the inverse of ``mx4_pack``."""
     _whole(t)
     index = _device(t.image)
-
-    def f(s):
-        codes = torch.empty((t.rows, t.K // 2), dtype=torch.uint8, device=index)
-        scales = torch.empty((t.rows, (t.K + 31) // 32), dtype=torch.uint8, device=index)
-        if t.rows:
-            _check(lib().w8a8_mx4_unpack(t.image.data_ptr(), t.rows, t.K, codes.data_ptr(), scales.data_ptr(),
-                                         s), "w8a8_mx4_unpack")
-        return codes, scales
-    return _call(index, stream, f)
+    if _elsewhere(index, stream):
+        with _there(index, stream):
+            return mx4_unpack(t)
+    s = _raw_stream(index)
+    codes = torch.empty((t.rows, t.K // 2), dtype=torch.uint8, device=index)
+    scales = torch.empty((t.rows, (t.K + 31) // 32), dtype=torch.uint8, device=index)
+    if t.rows:
+        _check(lib().w8a8_mx4_unpack(t.image.data_ptr(), t.rows, t.K, codes.data_ptr(), scales.data_ptr(),
+                                     s), "w8a8_mx4_unpack")
+    return codes, scales
 
 
 def mx4_dequant(t: MX4Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The values the image stands for, bf16 [..., K]."""
     _whole(t)
     index = _device(t.image, out)
-
-    def f(s):
-        x = _output(out, t.lead, t.K, index)
-        if t.rows:
-            _check(lib().w8a8_mx4_dequant(t.image.data_ptr(), t.rows, t.K, x.data_ptr(), s), "w8a8_mx4_dequant")
-        return x
-    return _call(index, stream, f)
+    if _elsewhere(index, stream):
+        with _there(index, stream):
+            return mx4_dequant(t, out)
+    s = _raw_stream(index)
+    x = _output(out, t.lead, t.K, index)
+    if t.rows:
+        _check(lib().w8a8_mx4_dequant(t.image.data_ptr(), t.rows, t.K, x.data_ptr(), s), "w8a8_mx4_dequant")
+    return x
 
 
 def mx4_scaled_mm(a: MX4Tensor, w: MX4Tensor, bias: Optional[torch.Tensor] = None,
@@ -208,15 +227,16 @@ def mx4_scaled_mm(a: MX4Tensor, w: MX4Tensor, bias: Optional[torch.Tensor] = Non
     _whole(a)
     _weight(w, bias, a.K)
     index = _device(a.image, w.image, bias, out)
-
-    def f(s):
-        M, N, K = a.rows, w.rows, a.K
-        y = _output(out, a.lead, N, index)
-        if M:
-            _check(lib().w8a8_mx4_scaled_mm(a.image.data_ptr(), w.image.data_ptr(), _at(bias), y.data_ptr(), M,
-                                            N, K, act, s), "w8a8_mx4_scaled_mm")
-        return y
-    return _call(index, stream, f)
+    if _elsewhere(index, stream):
+        with _there(index, stream):
+            return mx4_scaled_mm(a, w, bias, out, act=act)
+    s = _raw_stream(index)
+    M, N, K = a.rows, w.rows, a.K
+    y = _output(out, a.lead, N, index)
+    if M:
+        _check(lib().w8a8_mx4_scaled_mm(a.image.data_ptr(), w.image.data_ptr(), _at(bias), y.data_ptr(), M,
+                                        N, K, act, s), "w8a8_mx4_scaled_mm")
+    return y
 
 
 def mx4_scaled_mm_quant(a: MX4Tensor, w: MX4Tensor, bias: Optional[torch.Tensor] = None,
@@ -226,16 +246,17 @@ def mx4_scaled_mm_quant(a: MX4Tensor, w: MX4Tensor, bias: Optional[torch.Tensor]
     _whole(a)
     _weight(w, bias, a.K)
     index = _device(a.image, w.image, bias, image)
-
-    def f(s):
-        M, N, K = a.rows, w.rows, a.K
-        y = _image(image, M, N, index)
-        if M:
-            _check(lib().w8a8_mx4_scaled_mm_quant(a.image.data_ptr(), w.image.data_ptr(), _at(bias),
-                                                  y.data_ptr(), y.numel(), M, N, K, act, s),
-                   "w8a8_mx4_scaled_mm_quant")
-        return MX4Tensor(y, a.lead, N)
-    return _call(index, stream, f)
+    if _elsewhere(index, stream):
+        with _there(index, stream):
+            return mx4_scaled_mm_quant(a, w, bias, image, act=act)
+    s = _raw_stream(index)
+    M, N, K = a.rows, w.rows, a.K
+    y = _image(image, M, N, index)
+    if M:
+        _check(lib().w8a8_mx4_scaled_mm_quant(a.image.data_ptr(), w.image.data_ptr(), _at(bias),
+                                              y.data_ptr(), y.numel(), M, N, K, act, s),
+               "w8a8_mx4_scaled_mm_quant")
+    return MX4Tensor(y, a.lead, N)
 
 
 def mx4_linear(x: torch.Tensor, w: MX4Tensor, bias: Optional[torch.Tensor] = None,
@@ -245,17 +266,18 @@ def mx4_linear(x: torch.Tensor, w: MX4Tensor, bias: Optional[torch.Tensor] = Non
     _need_cuda(x, "x", torch.bfloat16)
     _weight(w, bias, x.shape[-1])
     index = _device(x, w.image, bias, out, workspace)
-
-    def f(s):
-        x2, M, ldx = _rows_of(x)
-        N, K = w.rows, w.K
-        y = _output(out, x.shape[:-1], N, index)
-        if M:
-            ws, nbytes = _scratch(workspace, mx4_linear_workspace_bytes(M, N, K), index)
-            _check(lib().w8a8_mx4_linear(x2.data_ptr(), ldx, w.image.data_ptr(), _at(bias), y.data_ptr(), M, N,
-                                         K, act, _at(ws), nbytes, s), "w8a8_mx4_linear")
-        return y
-    return _call(index, stream, f)
+    if _elsewhere(index, stream):
+        with _there(index, stream):
+            return mx4_linear(x, w, bias, out, workspace, act=act)
+    s = _raw_stream(index)
+    x2, M, ldx = _rows_of(x)
+    N, K = w.rows, w.K
+    y = _output(out, x.shape[:-1], N, index)
+    if M:
+        ws, nbytes = _scratch(workspace, mx4_linear_workspace_bytes(M, N, K), index)
+        _check(lib().w8a8_mx4_linear(x2.data_ptr(), ldx, w.image.data_ptr(), _at(bias), y.data_ptr(), M, N,
+                                     K, act, _at(ws), nbytes, s), "w8a8_mx4_linear")
+    return y
 
 
 def mx4_linear_quant(x: torch.Tensor, w: MX4Tensor, bias: Optional[torch.Tensor] = None,
@@ -266,18 +288,19 @@ def mx4_linear_quant(x: torch.Tensor, w: MX4Tensor, bias: Optional[torch.Tensor]
     _need_cuda(x, "x", torch.bfloat16)
     _weight(w, bias, x.shape[-1])
     index = _device(x, w.image, bias, image, workspace)
-
-    def f(s):
-        x2, M, ldx = _rows_of(x)
-        N, K = w.rows, w.K
-        y = _image(image, M, N, index)
-        if M:
-            ws, nbytes = _scratch(workspace, mx4_linear_workspace_bytes(M, N, K), index)
-            _check(lib().w8a8_mx4_linear_quant(x2.data_ptr(), ldx, w.image.data_ptr(), _at(bias), y.data_ptr(),
-                                               y.numel(), M, N, K, act, _at(ws), nbytes, s),
-                   "w8a8_mx4_linear_quant")
-        return MX4Tensor(y, x.shape[:-1], N)
-    return _call(index, stream, f)
+    if _elsewhere(index, stream):
+        with _there(index, stream):
+            return mx4_linear_quant(x, w, bias, image, workspace, act=act)
+    s = _raw_stream(index)
+    x2, M, ldx = _rows_of(x)
+    N, K = w.rows, w.K
+    y = _image(image, M, N, index)
+    if M:
+        ws, nbytes = _scratch(workspace, mx4_linear_workspace_bytes(M, N, K), index)
+        _check(lib().w8a8_mx4_linear_quant(x2.data_ptr(), ldx, w.image.data_ptr(), _at(bias), y.data_ptr(),
+                                           y.numel(), M, N, K, act, _at(ws), nbytes, s),
+               "w8a8_mx4_linear_quant")
+    return MX4Tensor(y, x.shape[:-1], N)
 
 
 class MX4Linear:

@@ -1,17 +1,16 @@
 """The norms around a block with its gate and residual: the binding of ``w8a8_block_norm``."""
 from __future__ import annotations
 
-import ctypes
+import struct
 from typing import NamedTuple, Optional
 
 import torch
 
-from .binding import _P, _SZ, _check, _need_cuda, lib
-from .mx4 import MX4Tensor, _call, _device, _rows_of, mx4_bytes
+from .binding import _check, _need_cuda, lib
+from .mx4 import MX4Tensor, _bytes, _device, _elsewhere, _raw_stream, _rows_of, _there, mx4_bytes
 
 _KINDS = {"rms": 1, "layer": 2}
 _RESIDUAL = {torch.bfloat16: 0, torch.float32: 1}
-_I64 = ctypes.c_int64
 
 
 class Norm(NamedTuple):
@@ -31,31 +30,27 @@ class BlockNormOutput(NamedTuple):
     mx4: Optional[MX4Tensor]
 
 
-class _NormStruct(ctypes.Structure):
-    _fields_ = [("kind", ctypes.c_int), ("eps", ctypes.c_float), ("weight", _P), ("bias", _P)]
+#: w8a8_block_norm_args, field by field (native alignment).
+_ARGS = struct.Struct("@qq Pq PPqq if ifPP ifPP PPP qqq qq P Pq PP PN".replace(" ", ""))
 
 
-class _Args(ctypes.Structure):
-    _fields_ = [("M", _I64), ("K", _I64), ("x", _P), ("ldx", _I64), ("residual", _P),
-                ("residual_out", _P), ("ldr", _I64), ("ldro", _I64), ("residual_dtype", ctypes.c_int),
-                ("residual_scale", ctypes.c_float), ("post", _NormStruct), ("pre", _NormStruct),
-                ("gate", _P), ("scale", _P), ("shift", _P), ("ld_gate", _I64), ("ld_scale", _I64),
-                ("ld_shift", _I64), ("groups", _I64), ("rows_per_group", _I64), ("group_index", _P),
-                ("y", _P), ("ldy", _I64), ("q", _P), ("a_scale", _P), ("image", _P),
-                ("image_bytes", _SZ)]
+def _vectors(norm: Optional[Norm], K: int):
+    """(kind, eps, weight, bias) of a w8a8_norm."""
+    if norm is None:
+        return 0, 0.0, 0, 0
+    kind, weight, bias, eps = norm
+    if kind not in _KINDS:
+        raise ValueError(f"norm kind must be one of {sorted(_KINDS)}, got {kind!r}")
+    return _KINDS[kind], eps, _vector(weight, "norm weight", K), _vector(bias, "norm bias", K)
 
 
-def _set_norm(to: _NormStruct, norm: Norm, K: int):
-    kind = _KINDS.get(norm.kind)
-    if kind is None:
-        raise ValueError(f"norm kind must be one of {sorted(_KINDS)}, got {norm.kind!r}")
-    to.kind, to.eps = kind, norm.eps
-    for name, t in (("weight", norm.weight), ("bias", norm.bias)):
-        if t is not None:
-            _need_cuda(t, f"norm {name}", torch.bfloat16)
-            if t.numel() != K or not t.is_contiguous():
-                raise ValueError(f"norm {name} must be contiguous and hold {K} values")
-            setattr(to, name, t.data_ptr())
+def _vector(t: Optional[torch.Tensor], name: str, K: int) -> int:
+    if t is None:
+        return 0
+    _need_cuda(t, name, torch.bfloat16)
+    if t.numel() != K or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and hold {K} values")
+    return t.data_ptr()
 
 
 def block_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, *, post: Optional[Norm] = None,
@@ -102,68 +97,66 @@ def block_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, *, post
     want_y = pre is not None and (codes is None if y is None else y)
     if pre is not None and codes is None and not want_y:
         raise ValueError("y=False leaves no output for the norm: ask for codes")
+    if _elsewhere(index, stream):
+        with _there(index, stream):
+            return block_norm(x, residual, post=post, gate=gate, residual_scale=residual_scale, pre=pre,
+                              scale=scale, shift=shift, rows_per_group=rows_per_group,
+                              group_index=group_index, codes=codes, y=y, residual_out=residual_out)
+    x2, M, ldx = _rows_of(x)
+    plain = x2 is x  # contiguous
+    r2 = new = None
+    ldr = ldro = dtype = 0
+    if residual is not None:
+        r2, _, ldr = _rows_of(residual)
+        dtype, ldro = _RESIDUAL[residual.dtype], K
+        if residual_out is None:
+            new = torch.empty_like(r2) if r2 is residual else torch.empty(x.shape, dtype=r2.dtype, device=index)
+        else:  # written in place: a view, never a copy
+            new = residual_out
+            n2 = new.view(-1, K) if new.is_contiguous() else new
+            if n2.dim() != 2 or (M and n2.stride(1) != 1):
+                raise ValueError("residual_out must be contiguous, or [rows, K] with unit stride along K")
+            if M > 1:
+                ldro = n2.stride(0)
 
-    def f(s):
-        x2, M, ldx = _rows_of(x)
-        a = _Args(M=M, K=K, x=x2.data_ptr(), ldx=ldx, residual_scale=residual_scale)
-        if post is not None:
-            _set_norm(a.post, post, K)
-        if pre is not None:
-            _set_norm(a.pre, pre, K)
-        new = None
-        held = [x2]  # what a copy was made of, until the launch
-        if residual is not None:
-            r2, _, a.ldr = _rows_of(residual)
-            held.append(r2)
-            if residual_out is None:
-                new, a.ldro = torch.empty(x.shape, dtype=residual.dtype, device=index), K
-            else:  # written in place: a view, never a copy
-                new = residual_out
-                n2 = new.view(-1, K) if new.is_contiguous() else new
-                if n2.dim() != 2 or (M and n2.stride(1) != 1):
-                    raise ValueError("residual_out must be contiguous, or [rows, K] with unit stride along K")
-                a.ldro = n2.stride(0) if M > 1 else K
-            a.residual, a.residual_out = r2.data_ptr(), new.data_ptr()
-            a.residual_dtype = _RESIDUAL[residual.dtype]
+    groups, held, places = 0, [], []
+    for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
+        if t is None:
+            places.append((0, 0))
+            continue
+        _need_cuda(t, name, torch.bfloat16)
+        if t.dim() == 1:
+            t = t.view(1, -1)
+        if t.dim() != 2 or t.shape[1] != K or (groups and t.shape[0] != groups):
+            raise ValueError(f"{name} must be [groups, {K}], with as many groups as the others, "
+                             f"got {list(t.shape)}")
+        t, groups, ld = _rows_of(t)
+        held.append(t)  # what a copy was made of, until the launch
+        places.append((t.data_ptr(), ld))
+    if group_index is not None:
+        _need_cuda(group_index, "group_index", torch.int32)
+        if group_index.numel() != M or not group_index.is_contiguous():
+            raise ValueError(f"group_index must be contiguous and hold {M} values")
+        groups = groups or 1
+    if rows_per_group is None:
+        rows_per_group = M or 1
 
-        groups = 0
-        for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
-            if t is None:
-                continue
-            _need_cuda(t, name, torch.bfloat16)
-            if t.dim() == 1:
-                t = t.view(1, -1)
-            if t.dim() != 2 or t.shape[1] != K or (groups and t.shape[0] != groups):
-                raise ValueError(f"{name} must be [groups, {K}], with as many groups as the others, "
-                                 f"got {list(t.shape)}")
-            t, groups, ld = _rows_of(t)
-            held.append(t)
-            setattr(a, name, t.data_ptr())
-            setattr(a, "ld_" + name, ld)
-        if group_index is not None:
-            _need_cuda(group_index, "group_index", torch.int32)
-            if group_index.numel() != M or not group_index.is_contiguous():
-                raise ValueError(f"group_index must be contiguous and hold {M} values")
-            a.group_index = group_index.data_ptr()
-            groups = groups or 1
-        if groups:
-            a.groups = groups
-            a.rows_per_group = (M or 1) if rows_per_group is None else rows_per_group
-
-        out = q = a_scale = image = None
-        if want_y:
-            out = torch.empty(x.shape, dtype=torch.bfloat16, device=index)
-            a.y, a.ldy = out.data_ptr(), K
-        if codes == "int8":
-            q = torch.empty(x.shape, dtype=torch.int8, device=index)
-            a_scale = torch.empty((M,), dtype=torch.float32, device=index)
-            a.q, a.a_scale = q.data_ptr(), a_scale.data_ptr()
-        elif codes == "mx4":
-            a.image_bytes = mx4_bytes(M, K) if M else 0
-            image = torch.empty((a.image_bytes,), dtype=torch.uint8, device=index)
-            a.image = image.data_ptr()
-        if M:
-            _check(lib().w8a8_block_norm(ctypes.byref(a), s), "w8a8_block_norm")
-        return BlockNormOutput(new, out, q, a_scale,
-                               None if image is None else MX4Tensor(image, x.shape[:-1], K))
-    return _call(index, stream, f)
+    out = q = a_scale = image = None
+    if want_y:
+        out = torch.empty_like(x) if plain else torch.empty(x.shape, dtype=torch.bfloat16, device=index)
+    if codes == "int8":
+        q = torch.empty(x.shape, dtype=torch.int8, device=index)
+        a_scale = torch.empty_strided((M,), (1,), dtype=torch.float32, device=index)
+    elif codes == "mx4":
+        image = _bytes(mx4_bytes(M, K) if M else 0, index)
+    if M:
+        args = _ARGS.pack(
+            M, K, x2.data_ptr(), ldx, 0 if r2 is None else r2.data_ptr(), 0 if new is None else new.data_ptr(),
+            ldr, ldro, dtype, residual_scale, *_vectors(post, K), *_vectors(pre, K),
+            places[0][0], places[1][0], places[2][0], places[0][1], places[1][1], places[2][1],
+            groups, rows_per_group, 0 if group_index is None else group_index.data_ptr(),
+            0 if out is None else out.data_ptr(), K, 0 if q is None else q.data_ptr(),
+            0 if a_scale is None else a_scale.data_ptr(), 0 if image is None else image.data_ptr(),
+            0 if image is None else image.numel())
+        _check(lib().w8a8_block_norm(args, _raw_stream(index)), "w8a8_block_norm")
+    return BlockNormOutput(new, out, q, a_scale, None if image is None else MX4Tensor(image, x.shape[:-1], K))
