@@ -11,7 +11,9 @@ its "Common Failures" table lists the output-rank collapse this avoids).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -130,6 +132,67 @@ def _need_cuda(t: torch.Tensor, name: str, dtype=None):
         raise ValueError(f"{name} must be a CUDA tensor")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+
+
+# ---- calls on the tensors' own device ---------------------------------------
+def _device(first: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
+    """The index of the one CUDA device that all the tensors given are on."""
+    index = first.get_device()
+    if index < 0:
+        raise ValueError("tensors must be CUDA tensors")
+    for t in others:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
+    return index
+
+
+def _elsewhere(index: int, stream) -> bool:
+    """Whether a call goes to another device than the current one or to a stream of its own."""
+    return stream is not None or index != torch.cuda.current_device()
+
+
+@contextlib.contextmanager
+def _there(index: int, stream):
+    """That device and stream made current: what the call allocates is that stream's."""
+    with torch.cuda.device(index):
+        if stream is None:
+            yield
+            return
+        if stream.device.index != index:
+            raise ValueError(f"stream of {stream.device}, tensors on cuda:{index}")
+        with torch.cuda.stream(stream):
+            yield
+
+
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _bytes(n: int, index: int) -> torch.Tensor:
+    return torch.empty_strided((n,), (1,), dtype=torch.uint8, device=index)
+
+
+@functools.lru_cache(maxsize=4096)
+def _size(name: str, device: int, *shape: int) -> int:
+    out = _SZ()
+    _check(getattr(lib(), name)(*shape, ctypes.byref(out)), name)
+    return out.value
+
+
+def _rows_of(x: torch.Tensor) -> Tuple[torch.Tensor, int, int]:
+    """[..., K] -> ([rows, K] with unit stride along K and rows on 16-byte boundaries, rows, row stride)."""
+    K = x.shape[-1]
+    if x.is_contiguous():
+        return x, x.numel() // K if K else 0, K
+    x2 = x if x.dim() == 2 else x.reshape(-1, K)
+    rows, (ld, step) = x2.shape[0], x2.stride()
+    if step != 1 or (rows > 1 and (ld % 8 or ld < K)):
+        x2 = x2.clone(memory_format=torch.contiguous_format)
+        ld = K
+    return x2, rows, ld if rows > 1 else K
+
+
+def _at(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
 
 
 # ---- sizes -------------------------------------------------------------------
@@ -451,12 +514,31 @@ class W8A8Linear:
 
     def apply_codes(self, q: torch.Tensor, a_scale: torch.Tensor,
                     out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-        """The layer on activations that are codes already (int8 [..., K] and their fp32
-        scales, as ``quant_act`` or ``block_norm`` forms them): y bf16 [..., N]."""
-        lead = q.shape[:-1]
-        y = scaled_mm(q.reshape(-1, self.K), a_scale, self.packed, self.w_scale, self.bias, self.N,
-                      out=out, stream=stream, act=self.act)
-        return y.view(*lead, self.N)
+        """The layer on activations that are codes already (int8 [..., K] and one fp32 scale
+        a row, as ``quant_act`` or ``block_norm`` forms them): y bf16 [..., N]."""
+        _need_cuda(q, "q", torch.int8)
+        _need_cuda(a_scale, "a_scale", torch.float32)
+        index = _device(q, a_scale, self.packed, out)
+        if q.shape[-1] != self.K or not q.is_contiguous():
+            raise ValueError(f"q must be contiguous [..., {self.K}], got {list(q.shape)}")
+        M = q.numel() // self.K
+        if a_scale.numel() != M or not a_scale.is_contiguous():
+            raise ValueError(f"a_scale must be contiguous and hold {M} values")
+        if _elsewhere(index, stream):
+            with _there(index, stream):
+                return self.apply_codes(q, a_scale, out)
+        if out is None:
+            out = torch.empty((*q.shape[:-1], self.N), dtype=torch.bfloat16, device=index)
+        elif out.dtype != torch.bfloat16 or out.numel() != M * self.N or not out.is_contiguous():
+            raise ValueError(f"out must be contiguous bf16 and hold [{M}, {self.N}]")
+        if M:
+            need = _size("w8a8_scaled_mm_workspace_bytes", index, M, self.N, self.K)
+            ws = _bytes(need, index) if need else None
+            _check(lib().w8a8_scaled_mm_act(q.data_ptr(), a_scale.data_ptr(), self.packed.data_ptr(),
+                                            self.w_scale.data_ptr(), _at(self.bias), out.data_ptr(), M,
+                                            self.N, self.K, self.act, _at(ws), need, _raw_stream(index)),
+                   "w8a8_scaled_mm_act")
+        return out.view(*q.shape[:-1], self.N)
 
     def split(self, y: torch.Tensor):
         return torch.split(y, list(self.splits), dim=-1)

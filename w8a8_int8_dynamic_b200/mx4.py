@@ -7,58 +7,13 @@ rows returns an empty result without a launch.
 """
 from __future__ import annotations
 
-import contextlib
-import ctypes
-import functools
 import math
 from typing import Optional, Tuple
 
 import torch
 
-from .binding import ACT_NONE, _SZ, _check, _need_cuda, lib
-
-
-def _device(first: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
-    """The index of the one CUDA device that all the tensors given are on."""
-    index = first.get_device()
-    if index < 0:
-        raise ValueError("tensors must be CUDA tensors")
-    for t in others:
-        if t is not None and t.get_device() != index:
-            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
-    return index
-
-
-def _elsewhere(index: int, stream) -> bool:
-    """Whether a call goes to another device than the current one or to a stream of its own."""
-    return stream is not None or index != torch.cuda.current_device()
-
-
-@contextlib.contextmanager
-def _there(index: int, stream):
-    """That device and stream made current: what the call allocates is that stream's."""
-    with torch.cuda.device(index):
-        if stream is None:
-            yield
-            return
-        if stream.device.index != index:
-            raise ValueError(f"stream of {stream.device}, tensors on cuda:{index}")
-        with torch.cuda.stream(stream):
-            yield
-
-
-_raw_stream = torch._C._cuda_getCurrentRawStream
-
-
-def _bytes(n: int, index: int) -> torch.Tensor:
-    return torch.empty_strided((n,), (1,), dtype=torch.uint8, device=index)
-
-
-@functools.lru_cache(maxsize=4096)
-def _size(name: str, device: int, *shape: int) -> int:
-    out = _SZ()
-    _check(getattr(lib(), name)(*shape, ctypes.byref(out)), name)
-    return out.value
+from .binding import (ACT_NONE, _at, _bytes, _check, _device, _elsewhere, _need_cuda, _raw_stream, _rows_of,
+                      _size, _there, lib)
 
 
 def mx4_bytes(rows: int, K: int) -> int:
@@ -89,22 +44,6 @@ class MX4Tensor:
 
     def unpack(self, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
         return mx4_unpack(self, stream=stream)
-
-
-def _rows_of(x: torch.Tensor) -> Tuple[torch.Tensor, int, int]:
-    """[..., K] -> ([rows, K] with unit stride along K and rows on 16-byte boundaries, rows, row stride)."""
-    K = x.shape[-1]
-    if x.is_contiguous():
-        return x, x.numel() // K if K else 0, K
-    x2 = x.reshape(-1, K)
-    rows = x2.shape[0]
-    if x2.stride(1) != 1 or (rows > 1 and (x2.stride(0) % 8 or x2.stride(0) < K)):
-        x2 = x2.clone(memory_format=torch.contiguous_format)
-    return x2, rows, x2.stride(0) if rows > 1 else K
-
-
-def _at(t: Optional[torch.Tensor]) -> Optional[int]:
-    return None if t is None else t.data_ptr()
 
 
 def _image(image: Optional[torch.Tensor], rows: int, K: int, index: int) -> torch.Tensor:

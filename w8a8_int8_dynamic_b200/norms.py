@@ -6,8 +6,8 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from .binding import _check, _need_cuda, lib
-from .mx4 import MX4Tensor, _bytes, _device, _elsewhere, _raw_stream, _rows_of, _there, mx4_bytes
+from .binding import _bytes, _check, _device, _elsewhere, _need_cuda, _raw_stream, _rows_of, _there, lib
+from .mx4 import MX4Tensor, mx4_bytes
 
 _KINDS = {"rms": 1, "layer": 2}
 _RESIDUAL = {torch.bfloat16: 0, torch.float32: 1}
@@ -127,9 +127,10 @@ def block_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, *, post
         _need_cuda(t, name, torch.bfloat16)
         if t.dim() == 1:
             t = t.view(1, -1)
-        if t.dim() != 2 or t.shape[1] != K or (groups and t.shape[0] != groups):
+        shape = t.shape
+        if len(shape) != 2 or shape[1] != K or (groups and shape[0] != groups):
             raise ValueError(f"{name} must be [groups, {K}], with as many groups as the others, "
-                             f"got {list(t.shape)}")
+                             f"got {list(shape)}")
         t, groups, ld = _rows_of(t)
         held.append(t)  # what a copy was made of, until the launch
         places.append((t.data_ptr(), ld))
