@@ -6,7 +6,7 @@
 // 32 or 64 of them) its N operand.  A pipeline stage is one weight tile (17 KB,
 // one copy, codes and scales) and the rows' codes of the same 256 elements.
 //
-// Work split: a cluster of C CTAs (1, 2 or 4) takes a 128-row weight slab,
+// Work split: a cluster of C CTAs (1 to 4) takes a 128-row weight slab,
 // each CTA a C-th of its K; clusters are persistent over the slabs.  The
 // partial sums are joined through distributed shared memory: the rows of x are
 // finished in chunks of 16, chunk q by the CTA of rank q mod C; the others send
@@ -40,7 +40,7 @@ struct StreamCfg {
   static constexpr int kS = kQ + NT * 128;            // their scales
   static constexpr int kStageBytes = kS + kMxScaleBytes;  // a multiple of 1024
   static constexpr int kRecv = kStages * kStageBytes;  // the parts of the cluster's CTAs
-  static constexpr int kBars = kRecv + 4 * 16 * 128 * 4;  // C x ceil(NT / 16 / C) chunks: at most 4
+  static constexpr int kBars = kRecv + 4 * 16 * 128 * 4;  // C * ceil(NT / 16 / C) chunks: at most 4
   // full[S], empty[S], tfull[2], tempty[2], recv, sent, done
   static constexpr int kMisc = kBars + (2 * kStages + 7) * 8;
   static constexpr int kAlloc = kMisc + 16 + 1024;
@@ -55,13 +55,14 @@ struct StreamArgs {
   const uint16_t *x;  // QUANT
   int64_t ldx;
   int K;
-  int C;              // CTAs of a cluster: 1, 2 or 4
+  int C;              // CTAs of a cluster: 1 to 4
   int slabs;          // 128-row slabs of the weight
 };
 
 // Bytes a microsecond that DRAM delivers, and that one SM's copies do.
 constexpr double kDramBytesPerUs = 6.5e6, kSmBytesPerUs = 8e4, kJoinUs = 1.0;
 
+constexpr int kMaxCluster = 4;
 constexpr int kPrefetchTiles = 16;  // 272 KB a CTA, 40 MB in all
 constexpr int kStreamThreads = 192;
 constexpr int kQuantWarps = 8;
@@ -132,7 +133,7 @@ __global__ void __launch_bounds__(kStreamThreads + (QUANT ? 32 * kQuantWarps : 0
 
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int C = args.C, log_c = C == 4 ? 2 : C - 1;
+  const int C = args.C;
   const int rank = C > 1 ? (int)cluster_ctarank() : 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -286,13 +287,13 @@ __global__ void __launch_bounds__(kStreamThreads + (QUANT ? 32 * kQuantWarps : 0
         // (they have read the previous ones)
         if (i > 0 && !(wait(sent, (uint32_t)(i - 1) & 1) && acquire_cluster(sent, (uint32_t)(i - 1) & 1))) break;
         for (int q = 0; q < chunks; ++q) {
-          const int to = q & (C - 1);
+          const int to = q % C;
           if (to == rank) continue;
           uint32_t v[16];
           tmem_ld_32x32b_x16(taddr + q * 16, v);
           tmem_ld_wait();
           const uint32_t at = map_to_cta(parts_addr, (uint32_t)to) +
-                              (uint32_t)(((q >> log_c) * C + rank) * (16 * 512));
+                              (uint32_t)((q / C * C + rank) * (16 * 512));
 #pragma unroll
           for (int m = 0; m < 16; ++m)
             if (q * 16 + m < M) st_cluster_f32(at + m * 512, __uint_as_float(v[m]));
@@ -309,7 +310,7 @@ __global__ void __launch_bounds__(kStreamThreads + (QUANT ? 32 * kQuantWarps : 0
       // time 22.7 us, eight 20.0, sixteen 18.2).
       for (int q = rank; q < chunks; q += C) {
         const int m0 = q * 16, rows = min(16, M - m0);
-        float *part = parts + (C > 1 ? (q >> log_c) * C : 0) * (16 * 128);
+        float *part = parts + (C > 1 ? q / C * C : 0) * (16 * 128);
         {
           uint32_t v[16];
           tmem_ld_32x32b_x16(taddr + m0, v);
@@ -425,24 +426,24 @@ cudaError_t allow_smem() {
   });
 }
 
-// Clusters of 2^i CTAs that the device holds at once (0: not that size), asked
+// Clusters of C CTAs that the device holds at once (0: not that size), asked
 // once per device.  Of the instance without QUANT for both, so that the layer
 // splits K, and rounds its sums, as the product on codes does.
 template <int NT>
-int max_clusters(int i) {
+int max_clusters(int C) {
   constexpr int kDevices = 64;
-  static std::atomic<int> known[kDevices][3];  // + 1
+  static std::atomic<int> known[kDevices][kMaxCluster + 1];  // + 1
   const int dev = current_device();
   const bool keep = dev >= 0 && dev < kDevices;
-  int n = keep ? known[dev][i].load(std::memory_order_relaxed) - 1 : -1;
+  int n = keep ? known[dev][C].load(std::memory_order_relaxed) - 1 : -1;
   if (n >= 0) return n;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(1u << i);
+  cfg.gridDim = dim3((unsigned)C);
   cfg.blockDim = dim3(kStreamThreads);
   cfg.dynamicSmemBytes = StreamCfg<NT>::kAlloc;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 1u << i;
+  attr[0].val.clusterDim.x = (unsigned)C;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
@@ -452,7 +453,7 @@ int max_clusters(int i) {
     (void)cudaGetLastError();
     return 0;
   }
-  if (keep) known[dev][i].store(n + 1, std::memory_order_relaxed);
+  if (keep) known[dev][C].store(n + 1, std::memory_order_relaxed);
   return n;
 }
 
@@ -464,10 +465,9 @@ w8a8_status run(StreamArgs a, cudaStream_t stream) {
   // the time to join a split slab.
   double best = 1e30;
   int best_clusters = 0;
-  for (int i = 0; i < 3; ++i) {
-    const int C = 1 << i;
-    if (C > a.p.kt) break;
-    const int clusters = max_clusters<NT>(i);
+  for (int C = 1; C <= kMaxCluster && C <= a.p.kt; ++C) {
+    // (the parts of 64 rows by three CTAs would not fit in shared memory)
+    const int clusters = C * ((NT / 16 + C - 1) / C) <= 4 ? max_clusters<NT>(C) : 0;
     if (clusters < 1) continue;
     const int tiles = (a.p.kt + C - 1) / C;
     auto round_us = [&](int n) {
