@@ -299,9 +299,9 @@ w8a8_status launch_mx4_1sm(const CUtensorMap &ty, Mx4Args a, cudaStream_t stream
                                     MxSmem::kAlloc);
       }) != cudaSuccess)
     return W8A8_ERR_CUDA;
-  a.tiles_m = (a.M + 127) / 128;
+  a.tiles_m = (int)mx4_slabs(a.M);
   // an output image's columns are written to the end of its last tile
-  a.tiles_n = a.y_image ? a.y_kt * (kMxTileK / kMxBN) : (a.N + kMxBN - 1) / kMxBN;
+  a.tiles_n = a.y_image ? a.y_kt * (kMxTileK / kMxBN) : (int)mx4_slabs(a.N);
   if ((int64_t)a.tiles_m * a.tiles_n > 0x7FFFFFFF) return W8A8_ERR_UNSUPPORTED_SHAPE;
   a.row_major = a.M > a.N ? 1 : 0;
   cudaLaunchConfig_t cfg = {};
@@ -339,7 +339,7 @@ bool use_pair(const Mx4Args &a) {
   if (p != 0) return true;
   auto rounds = [](int64_t tiles, int64_t slots) { return (double)((tiles + slots - 1) / slots); };
   const int64_t sms = sm_count();
-  const double pair = rounds(((a.M + 255) / 256) * (int64_t)((a.N + 255) / 256), sms / 2) * a.kt * 0.365 + 1.4;
+  const double pair = rounds((((int64_t)a.M + 255) / 256) * (((int64_t)a.N + 255) / 256), sms / 2) * a.kt * 0.365 + 1.4;
   const double single = rounds(mx4_slabs(a.M) * mx4_slabs(a.N), sms) * a.kt * 0.27;
   return pair < single;
 }

@@ -350,8 +350,8 @@ w8a8_status launch_mx4_pair(Mx4Args a, cudaStream_t stream) {
                                     PairSmem::kAlloc);
       }) != cudaSuccess)
     return W8A8_ERR_CUDA;
-  a.tiles_m = (a.M + 255) / 256;
-  a.tiles_n = (a.N + 255) / 256;
+  a.tiles_m = (int)(((int64_t)a.M + 255) / 256);
+  a.tiles_n = (int)(((int64_t)a.N + 255) / 256);
   a.row_major = a.M > a.N ? 1 : 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * std::max(1, std::min(a.tiles_m * a.tiles_n, sm_count() / 2))));
