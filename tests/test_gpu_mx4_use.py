@@ -1,0 +1,260 @@
+"""GPU tests of the 4-bit layers and the block norm as a serving program runs them: together, on other streams, in
+CUDA graphs, back to back, in place, with rows or values left out, and on tensors longer than 32-bit offsets reach."""
+import numpy as np
+import pytest
+import torch
+
+import mx4_ref as ref
+import w8a8_int8_dynamic_b200 as w8
+from gpu_util import require_gpu
+from test_gpu_mx4 import bf, check_product, f64, operands, plain, sample
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    require_gpu()
+    yield
+    assert w8.poll_status() == 0
+
+
+def layers(seed, D, F):
+    rng = np.random.default_rng(seed)
+    up = w8.MX4Linear.from_float(bf(rng.standard_normal((F, D)) * D ** -0.5), bf(rng.standard_normal(F) * 0.1),
+                                 act=w8.ACT_GELU_TANH)
+    down = w8.MX4Linear.from_float(bf(rng.standard_normal((D, F)) * F ** -0.5), bf(rng.standard_normal(D) * 0.1))
+    n = w8.Norm("layer", bf(1 + 0.1 * rng.standard_normal(D)), bf(0.1 * rng.standard_normal(D)))
+    mod = bf(rng.standard_normal((2, 3 * D)) * 0.3).split(D, 1)
+    return up, down, n, mod
+
+
+def block(x, stream, up, down, n, mod, per):
+    """A transformer block's second half: norm after attention into the stream, MLP, its norm into the stream."""
+    a = w8.block_norm(x, stream, gate=mod[0], pre=n, scale=mod[1], shift=mod[2], rows_per_group=per, codes="mx4")
+    h = up.quantised(a.mx4)
+    return w8.block_norm(down(h), a.residual, post=n, gate=mod[0], residual_scale=0.9, pre=n, rows_per_group=per)
+
+
+def block_in_steps(x, stream, up, down, n, mod, per):
+    """The same by unfused calls: each is tested against its formula elsewhere."""
+    a = w8.block_norm(x, stream, gate=mod[0], pre=n, scale=mod[1], shift=mod[2], rows_per_group=per)
+    y = w8.mx4_scaled_mm(w8.mx4_quant(a.y), up.w, up.bias, act=w8.ACT_GELU_TANH)
+    z = w8.mx4_scaled_mm(w8.mx4_quant(y), down.w, down.bias)
+    return w8.block_norm(z, a.residual, post=n, gate=mod[0], residual_scale=0.9, pre=n, rows_per_group=per)
+
+
+@pytest.mark.parametrize("M", [1, 5, 16, 17, 64, 65, 300, 1100])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_a_block_fused_equals_its_steps(M, dtype):
+    D, F = 1040, 2064
+    up, down, n, mod = layers(3, D, F)
+    x = sample(np.random.default_rng(M), M, D)
+    stream = torch.randn(M, D, device="cuda").to(dtype)
+    per = -(-M // 2)
+    got, want = block(x, stream, up, down, n, mod, per), block_in_steps(x, stream, up, down, n, mod, per)
+    assert torch.equal(got.residual, want.residual) and torch.equal(got.y, want.y)
+    # the products in the middle, against 64 bits
+    a = w8.block_norm(x, stream, gate=mod[0], pre=n, scale=mod[1], shift=mod[2], rows_per_group=per, codes="mx4").mx4
+    check_product(up(a), a, up.w, up.bias, w8.ACT_GELU_TANH)
+    h = up.quantised(a)
+    check_product(down(h), h, down.w, down.bias, w8.ACT_NONE)
+
+
+@pytest.mark.parametrize("M", [1, 16, 17, 500])
+def test_int8_layer_on_the_norms_codes(M):
+    D, N = 528, 1032
+    rng = np.random.default_rng(M)
+    layer = w8.W8A8Linear(torch.from_numpy(rng.integers(-127, 128, (N, D), dtype=np.int8)).cuda(),
+                          torch.rand(N, device="cuda") * 1e-2, bf(rng.standard_normal(N)))
+    x, n = sample(rng, M, D), w8.Norm("rms", bf(1 + 0.1 * rng.standard_normal(D)))
+    out = w8.block_norm(x.view(1, M, D), pre=n, codes="int8", y=True)
+    y = layer.apply_codes(out.q, out.a_scale)
+    assert y.shape == (1, M, N) and torch.equal(y, layer(out.y))
+
+
+@pytest.mark.parametrize("M", [1, 40, 700])
+def test_graphs_replayed_on_new_inputs_beside_each_other(M):
+    """Two captures of the same layers, replayed by turns on new inputs, with eager calls between them."""
+    D, F = 784, 1552
+    up, down, n, mod = layers(5, D, F)
+    rng = np.random.default_rng(M)
+    per = -(-M // 2)
+    held = []
+    for _ in range(2):
+        x, stream = sample(rng, M, D), torch.randn(M, D, device="cuda")
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            block(x, stream, up, down, n, mod, per)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            out = block(x, stream, up, down, n, mod, per)
+        held.append((g, x, stream, out))
+    for i in range(6):
+        g, x, stream, out = held[i % 2]
+        x.copy_(sample(rng, M, D))
+        stream.copy_(torch.randn(M, D, device="cuda"))
+        g.replay()
+        want = block(x, stream, up, down, n, mod, per)
+        torch.cuda.synchronize()
+        assert torch.equal(out.residual, want.residual) and torch.equal(out.y, want.y)
+    for g, *_ in held:
+        g.reset()
+
+
+@pytest.mark.parametrize("M", [3, 17, 300])
+def test_other_streams(M):
+    """Calls given a stream, from a thread whose current stream is another; one layer on two streams at once."""
+    D, F = 784, 1552
+    up, down, n, mod = layers(7, D, F)
+    x = sample(np.random.default_rng(M), M, D)
+    want = down(up.quantised(x))
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for s in (s1, s2):
+        s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for i in range(20):
+        for s in (s1, s2):
+            h = up.quantised(x, stream=s)
+            got.append(down(h, stream=s))
+            q = w8.mx4_quant(x, stream=s)
+            r = w8.block_norm(q.dequant(stream=s), pre=n, codes="mx4", stream=s)
+            got.append(w8.mx4_scaled_mm(r.mx4, up.w, stream=s))
+    torch.cuda.synchronize()
+    second = w8.mx4_scaled_mm(w8.block_norm(w8.mx4_quant(x).dequant(), pre=n, codes="mx4").mx4, up.w)
+    for i, y in enumerate(got):
+        assert torch.equal(y, second if i % 2 else want)
+
+
+def test_many_calls_back_to_back():
+    """Chains whose kernels start before the ones ahead have ended: every shape's kernel before and after every
+    other's, on memory that the allocator hands from one call to the next, weights made just before their use."""
+    rng = np.random.default_rng(11)
+    D = 784
+    cases = []
+    for M in (1, 16, 17, 33, 65, 130, 600):
+        for N in (136, 1040):
+            x, w, b = operands(M + N, M, N, D)
+            codes, scales = w.unpack()
+            cases.append((x, codes, scales, b, w8.mx4_linear(x, w, b)))
+    n = w8.Norm("rms")
+    torch.cuda.synchronize()
+    for _ in range(6):
+        order = rng.permutation(len(cases))
+        got = []
+        for i in order:
+            x, codes, scales, b, _ = cases[i]
+            w = w8.mx4_pack(codes, scales)
+            y = w8.mx4_linear(x, w, b)
+            w8.block_norm(x, pre=n, codes="mx4")
+            got.append((i, y))
+        torch.cuda.synchronize()
+        for i, y in got:
+            assert torch.equal(y, cases[i][4])
+
+
+def test_weights_that_the_kernel_ahead_has_just_written():
+    """The right operand may come from any kernel: a quantisation, a product's epilogue, a norm."""
+    x, w, _ = operands(13, 24, 528, 272, bias=False)
+    v = sample(np.random.default_rng(1), 272, 528)
+    n = w8.Norm("rms")
+    for _ in range(30):
+        for make in (lambda: w8.mx4_quant(v), lambda: w8.mx4_scaled_mm_quant(w8.mx4_quant(v), w8.mx4_quant(v[:, :528])),
+                     lambda: w8.block_norm(v, pre=n, codes="mx4").mx4):
+            t = make()
+            a = sample(np.random.default_rng(2), 5, t.K)
+            got = w8.mx4_linear(a, t)
+            torch.cuda.synchronize()
+            assert torch.equal(got, w8.mx4_linear(a, t))
+
+
+def test_nan_and_infinity_stay_in_their_rows():
+    for M in (5, 20, 200):
+        x, w, b = operands(M, M, 264, 528)
+        y = w8.mx4_linear(x, w, b)
+        x[1, 100], x[3, 527] = float("nan"), float("-inf")
+        got = w8.mx4_linear(x, w, b)
+        rest = [m for m in range(M) if m not in (1, 3)]
+        assert got[1].isnan().all() and got[3].isnan().all() and torch.equal(got[rest], y[rest])
+        # a row of zeros gives the bias
+        x[:] = 0
+        assert torch.equal(w8.mx4_linear(x, w, b), b.expand(M, -1))
+
+
+def test_no_rows_no_launch():
+    x, w, b = operands(1, 4, 264, 272)
+    before = w8.launch_count()
+    for lead in ((0,), (2, 0)):
+        e = x[:0].view(*lead, 272)
+        assert w8.mx4_linear(e, w, b).shape == (*lead, 264)
+        t = w8.mx4_quant(e)
+        assert t.dequant().shape == e.shape and w8.mx4_scaled_mm(t, w, b).shape == (*lead, 264)
+        assert w8.mx4_scaled_mm_quant(t, w, b[:264]).lead == lead if w.rows % 16 == 0 else True
+        assert w8.block_norm(e, e.float(), pre=w8.Norm("rms"), codes="int8").q.shape == e.shape
+    assert w8.launch_count() == before
+
+
+def test_one_launch_a_few_row_layer_and_two_a_larger_one():
+    x, w, b = operands(1, 17, 264, 272)
+    for M, launches in ((1, 1), (16, 1), (17, 2)):
+        before = w8.launch_count()
+        w8.mx4_linear(x[:M], w, b)
+        assert w8.launch_count() - before == launches
+
+
+def test_outputs_given_and_refused():
+    x, w, b = operands(2, 20, 272, 272)
+    want = w8.mx4_linear(x, w, b)
+    out = torch.empty(20 * 272, dtype=torch.bfloat16, device="cuda")
+    assert torch.equal(w8.mx4_linear(x, w, b, out=out), want) and torch.equal(out.view(20, 272), want)
+    ws = torch.empty(w8.mx4_linear_workspace_bytes(20, 272, 272), dtype=torch.uint8, device="cuda")
+    assert torch.equal(w8.mx4_linear(x, w, b, workspace=ws), want)
+    t = w8.mx4_quant(x)
+    for f in (lambda: w8.mx4_linear(x, w, b, out=out.float()), lambda: w8.mx4_linear(x, w, b[:8]),
+              lambda: w8.mx4_linear(x.float(), w, b), lambda: w8.mx4_linear(x[:, :256], w, b),
+              lambda: w8.mx4_scaled_mm(t, w, b, out=torch.empty(272, 20, dtype=torch.bfloat16, device="cuda").t()),
+              lambda: w8.mx4_scaled_mm(w8.MX4Tensor(t.image[:100], (20,), 272), w, b),
+              lambda: w8.mx4_pack(*w.unpack()[:1], torch.zeros(272, 8, dtype=torch.uint8, device="cuda")),
+              lambda: w8.block_norm(x, x[:4], pre=w8.Norm("rms")), lambda: w8.block_norm(x),
+              lambda: w8.block_norm(x, pre=w8.Norm("batch")), lambda: w8.block_norm(x, pre=w8.Norm("rms"), codes="fp8"),
+              lambda: w8.block_norm(x, pre=w8.Norm("rms"), gate=b), lambda: w8.block_norm(x, x.double(), pre=w8.Norm("rms")),
+              lambda: w8.block_norm(x, pre=w8.Norm("rms"), y=False), lambda: w8.block_norm(x, x, scale=b),
+              lambda: w8.block_norm(x, x, gate=b.view(1, -1).expand(2, -1), pre=w8.Norm("rms"),
+                                    scale=b.view(1, -1).expand(3, -1))):
+        with pytest.raises(ValueError):
+            f()
+    for f in (lambda: w8.mx4_linear(x, w, b, workspace=ws[:16]), lambda: w8.mx4_quant(x, image=t.image[:16]),
+              lambda: w8.mx4_quant(x[:, :40]), lambda: w8.block_norm(x, x, gate=b.expand(2, -1), rows_per_group=3)):
+        with pytest.raises(w8.W8A8Error):
+            f()
+
+
+def test_offsets_past_32_bits():
+    """Images, streams and codes of more than 2^32 bytes: their last rows equal those of a call on these alone."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rows, K = 66000, 131072
+    x = torch.randn(rows, K, device="cuda", generator=g, dtype=torch.bfloat16)
+    assert w8.mx4_bytes(rows, K) > 1 << 32
+    t = w8.mx4_quant(x)
+    tail = slice(rows - 200, rows)
+    want = w8.mx4_quant(x[tail])
+    back = t.dequant()
+    assert torch.equal(back[tail], want.dequant()) and torch.equal(back[:100], w8.mx4_quant(x[:100]).dequant())
+    del back
+    w = w8.mx4_quant(torch.randn(16, K, device="cuda", generator=g).mul_(K ** -0.5).bfloat16())
+    y = w8.mx4_scaled_mm(t, w)
+    check_product(y[tail], want, w, None, w8.ACT_NONE)
+    # as the right operand: many output columns
+    a = w8.mx4_quant(x[:3])
+    z = w8.mx4_scaled_mm(a, t)
+    check_product(z[:, tail], a, want, None, w8.ACT_NONE)
+    del x, t, y, z
+    M, D = 300000, 8192
+    x = torch.randn(M, D, device="cuda", generator=g, dtype=torch.bfloat16)
+    n = w8.Norm("layer", bf(1 + 0.1 * np.random.default_rng(0).standard_normal(D)))
+    tail = slice(M - 300, M)
+    small = w8.block_norm(x[tail], x[tail].float(), pre=n, post=n, codes="int8", y=True)
+    big = w8.block_norm(x, x.float(), pre=n, post=n, codes="int8", y=True)
+    for name in ("residual", "y", "q", "a_scale"):
+        assert torch.equal(getattr(big, name)[tail], getattr(small, name))
