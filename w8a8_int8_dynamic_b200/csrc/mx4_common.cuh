@@ -220,7 +220,8 @@ w8a8_status launch_mx4_stream(const Mx4Args &p, const void *x, int64_t ldx, int6
 w8a8_status launch_mx4_pair(Mx4Args a, cudaStream_t stream);
 
 // The bias, activation and rounding of 8 consecutive outputs of a row.
-__device__ __forceinline__ uint4 mx4_finish8(const uint32_t *acc, const uint16_t *bias, int act) {
+template <int ACT>
+__device__ __forceinline__ uint4 mx4_finish8(const uint32_t *acc, const uint16_t *bias) {
   float t[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) t[i] = __uint_as_float(acc[i]);
@@ -231,9 +232,9 @@ __device__ __forceinline__ uint4 mx4_finish8(const uint32_t *acc, const uint16_t
     t[2 * h] = __fadd_rn(t[2 * h], __uint_as_float(bw[h] << 16));
     t[2 * h + 1] = __fadd_rn(t[2 * h + 1], __uint_as_float(bw[h] & 0xFFFF0000u));
   }
-  if (act != W8A8_ACT_NONE) {
+  if (ACT != W8A8_ACT_NONE) {
 #pragma unroll
-    for (int h = 0; h < 4; ++h) apply_act_pair(t[2 * h], t[2 * h + 1], act);
+    for (int h = 0; h < 4; ++h) apply_act_pair(t[2 * h], t[2 * h + 1], ACT);
   }
   uint32_t r[4];
 #pragma unroll

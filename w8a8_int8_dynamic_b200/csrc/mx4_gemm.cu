@@ -11,7 +11,10 @@
 // epilogue: bias, optional GELU, one rounding to bf16, then either TMA stores
 // of y or, for a layer that feeds another 4-bit layer, the MX codes of y.
 // A thread of the epilogue holds 32 consecutive outputs of one row, which is
-// one block: its maximum, scale and codes need no other thread.
+// one block: its maximum, scale and codes need no other thread.  Activation
+// and form of the output are fixed at compile time: with both in one kernel the
+// epilogue jumped over the code of the other forms, and fetching instructions
+// cost 0.5 to 1 us a launch (256 x 4096 x 4096: 11.3 us, now 10.0).
 //
 // Scale columns: every stage has its own TMEM columns (16: two groups of four
 // for either operand), written when the stage's MMAs are issued, so they are
@@ -53,6 +56,9 @@ __device__ __forceinline__ void mx4_tile_coords(const Mx4Args &a, int tile, int 
   }
 }
 
+// ACT, IMAGE: the activation (a w8a8_act) and the form of the output, fixed so
+// that the epilogue's code is short.
+template <int ACT, bool IMAGE>
 __global__ void __maxnreg__(kGemmRegs)
     mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_y, const Mx4Args args) {
   using L = MxSmem;
@@ -222,7 +228,7 @@ __global__ void __maxnreg__(kGemmRegs)
     const EpiWarp ew(warp);
     uint16_t *s_bias = reinterpret_cast<uint16_t *>(smem + L::kBias) + (warp - 2) * kCols;
     uint8_t *stage = smem + L::kOut + (warp - 2) * kEpiStagePerWarp;
-    const int n_end = args.y_image ? args.y_kt * kMxTileK : args.N;
+    const int n_end = IMAGE ? args.y_kt * kMxTileK : args.N;
     for (int i = 0; i < my_tiles; ++i) {
       int mb, nb;
       mx4_tile_coords(args, slot + i * nslots, mb, nb);
@@ -246,9 +252,9 @@ __global__ void __maxnreg__(kGemmRegs)
           [&](const uint32_t(&v)[32], int c) {
             uint4 out[4];
 #pragma unroll
-            for (int g = 0; g < 4; ++g) out[g] = mx4_finish8(v + 8 * g, s_bias + c * 32 + 8 * g, args.act);
+            for (int g = 0; g < 4; ++g) out[g] = mx4_finish8<ACT>(v + 8 * g, s_bias + c * 32 + 8 * g);
             const int nc = n0 + c * 32;
-            if (args.y_image) {
+            if constexpr (IMAGE) {
 #pragma unroll
               for (int g = 0; g < 4; ++g)
                 if (nc + 8 * g >= args.N) out[g] = make_uint4(0, 0, 0, 0);
@@ -291,12 +297,16 @@ __global__ void __maxnreg__(kGemmRegs)
   }
 }
 
-FuncAttrOnce g_mx_smem_attr;
+FuncAttrOnce g_mx_smem_attr[4];
 
 w8a8_status launch_mx4_1sm(const CUtensorMap &ty, Mx4Args a, cudaStream_t stream) {
-  if (g_mx_smem_attr.ensure([] {
-        return cudaFuncSetAttribute(mx4_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    MxSmem::kAlloc);
+  const int form = (a.act != W8A8_ACT_NONE ? 1 : 0) + (a.y_image ? 2 : 0);
+  auto k = form == 0   ? mx4_gemm_kernel<W8A8_ACT_NONE, false>
+           : form == 1 ? mx4_gemm_kernel<W8A8_ACT_GELU_TANH, false>
+           : form == 2 ? mx4_gemm_kernel<W8A8_ACT_NONE, true>
+                       : mx4_gemm_kernel<W8A8_ACT_GELU_TANH, true>;
+  if (g_mx_smem_attr[form].ensure([&] {
+        return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, MxSmem::kAlloc);
       }) != cudaSuccess)
     return W8A8_ERR_CUDA;
   a.tiles_m = (int)mx4_slabs(a.M);
@@ -314,7 +324,7 @@ w8a8_status launch_mx4_1sm(const CUtensorMap &ty, Mx4Args a, cudaStream_t stream
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, mx4_gemm_kernel, ty, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k, ty, a);
   if (e == cudaSuccess) count_launch();
   return from_cuda(e);
 }
@@ -327,10 +337,10 @@ bool use_stream(int64_t M) {
 
 // Pairs with 256 x 256 tiles or single CTAs with 128 x 128 ones: by the rounds
 // of tiles, a step of K taking 0.365 us in the one and 0.27 us in the other
-// when all SMs are busy, and 1.4 us more to start and end the pair kernel.
-// Measured (pair, single): 512 x 4096 x 4096 13.1, 10.8 us; 1024 x 4096 x 4096
-// 13.5, 14.8; 256 x 12288 x 4096 13.9, 15.1; 2048^3 11.2, 10.2; 128 x 27648 x
-// 5120 23.4, 20.1; 4096 x 12288 x 4096 77, 99.
+// when all SMs are busy, and 1 us more to start and end the pair kernel.
+// Measured (pair, single): 512 x 4096 x 4096 13.7, 11.2 us; 1024 x 4096 x 4096
+// 14.4, 16.8; 256 x 12288 x 4096 13.2, 15.0; 300 x 5120 x 13824 23.2, 19.7;
+// 2048^3 9.9, 10.3; 128 x 27648 x 5120 23.1, 20.2; 4096 x 12288 x 4096 76, 98.
 bool use_pair(const Mx4Args &a) {
   const int p = forced_path();
   // (the pair kernel's box coordinates are 32-bit rows of 128 bytes)
@@ -339,7 +349,7 @@ bool use_pair(const Mx4Args &a) {
   if (p != 0) return true;
   auto rounds = [](int64_t tiles, int64_t slots) { return (double)((tiles + slots - 1) / slots); };
   const int64_t sms = sm_count();
-  const double pair = rounds((((int64_t)a.M + 255) / 256) * (((int64_t)a.N + 255) / 256), sms / 2) * a.kt * 0.365 + 1.4;
+  const double pair = rounds((((int64_t)a.M + 255) / 256) * (((int64_t)a.N + 255) / 256), sms / 2) * a.kt * 0.365 + 1.0;
   const double single = rounds(mx4_slabs(a.M) * mx4_slabs(a.N), sms) * a.kt * 0.27;
   return pair < single;
 }

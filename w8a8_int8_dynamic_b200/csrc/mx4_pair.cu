@@ -51,6 +51,10 @@ struct PairSmem {
 static_assert(PairSmem::kStageBytes % 1024 == 0 && PairSmem::kAlloc <= 232448, "one CTA's shared memory");
 static_assert(kScaleBase + kScaleSets * kScaleSetCols <= 512, "TMEM columns");
 
+// ACT, IMAGE: the activation (a w8a8_act) and the form of the output, fixed so
+// that the epilogue's code is short: it runs a few times a launch, and its
+// instructions are fetched for each (see mx4_gemm.cu).
+template <int ACT, bool IMAGE>
 __global__ void __maxnreg__(kGemmRegs)
     mx4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_w,
                     const __grid_constant__ CUtensorMap tmap_ws, const __grid_constant__ CUtensorMap tmap_y,
@@ -238,7 +242,7 @@ __global__ void __maxnreg__(kGemmRegs)
     const EpiWarp ew(warp);
     uint16_t *s_bias = reinterpret_cast<uint16_t *>(smem + L::kBias) + (warp - 2) * 128;
     uint8_t *stage = smem + L::kOut + (warp - 2) * kEpiStagePerWarp;
-    const int n_end = args.y_image ? args.y_kt * kMxTileK : args.N;
+    const int n_end = IMAGE ? args.y_kt * kMxTileK : args.N;
     for (int i = 0; i < my_tiles; ++i) {
       int mb, nb;
       coords(i, mb, nb);
@@ -267,8 +271,8 @@ __global__ void __maxnreg__(kGemmRegs)
         if (n0 >= n_end) return;
         uint4 out[4];
 #pragma unroll
-        for (int g = 0; g < 4; ++g) out[g] = mx4_finish8(v + 8 * g, s_bias + c * 32 + 8 * g, args.act);
-        if (args.y_image) {
+        for (int g = 0; g < 4; ++g) out[g] = mx4_finish8<ACT>(v + 8 * g, s_bias + c * 32 + 8 * g);
+        if constexpr (IMAGE) {
 #pragma unroll
           for (int g = 0; g < 4; ++g)
             if (n0 + 8 * g >= args.N) out[g] = make_uint4(0, 0, 0, 0);
@@ -331,7 +335,7 @@ __global__ void __maxnreg__(kGemmRegs)
   }
 }
 
-FuncAttrOnce g_mx_pair_attr;
+FuncAttrOnce g_mx_pair_attr[4];
 
 }  // namespace
 
@@ -345,9 +349,13 @@ w8a8_status launch_mx4_pair(Mx4Args a, cudaStream_t stream) {
       !make_tmap_u8_2d_plain(&tws, a.w, rows_w, 128, 128, kScaleRows128, 128))
     return W8A8_ERR_CUDA;
   if (a.y && !make_tmap_out_bf16(&ty, a.y, (uint64_t)a.M, (uint64_t)a.N)) return W8A8_ERR_CUDA;
-  if (g_mx_pair_attr.ensure([] {
-        return cudaFuncSetAttribute(mx4_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    PairSmem::kAlloc);
+  const int form = (a.act != W8A8_ACT_NONE ? 1 : 0) + (a.y_image ? 2 : 0);
+  auto k = form == 0   ? mx4_pair_kernel<W8A8_ACT_NONE, false>
+           : form == 1 ? mx4_pair_kernel<W8A8_ACT_GELU_TANH, false>
+           : form == 2 ? mx4_pair_kernel<W8A8_ACT_NONE, true>
+                       : mx4_pair_kernel<W8A8_ACT_GELU_TANH, true>;
+  if (g_mx_pair_attr[form].ensure([&] {
+        return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, PairSmem::kAlloc);
       }) != cudaSuccess)
     return W8A8_ERR_CUDA;
   a.tiles_m = (int)(((int64_t)a.M + 255) / 256);
@@ -367,7 +375,7 @@ w8a8_status launch_mx4_pair(Mx4Args a, cudaStream_t stream) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, mx4_pair_kernel, ta, tw, tws, ty, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k, ta, tw, tws, ty, a);
   if (e == cudaSuccess) count_launch();
   return from_cuda(e);
 }
