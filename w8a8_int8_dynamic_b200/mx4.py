@@ -202,20 +202,24 @@ def mx4_linear(x: torch.Tensor, w: MX4Tensor, bias: Optional[torch.Tensor] = Non
                out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                stream=None, act: int = ACT_NONE) -> torch.Tensor:
     """The whole layer: y[..., N] = x[..., K] quantised, times w (``act``: epilogue activation)."""
-    _need_cuda(x, "x", torch.bfloat16)
     _weight(w, bias, x.shape[-1])
+    return _linear(x, w, bias, out, workspace, stream, act)
+
+
+def _linear(x, w, bias, out, workspace, stream, act):
+    """``mx4_linear`` with a weight and bias that have been checked."""
+    _need_cuda(x, "x", torch.bfloat16)
     index = _device(x, w.image, bias, out, workspace)
     if _elsewhere(index, stream):
         with _there(index, stream):
-            return mx4_linear(x, w, bias, out, workspace, act=act)
-    s = _raw_stream(index)
+            return _linear(x, w, bias, out, workspace, None, act)
     x2, M, ldx = _rows_of(x)
     N, K = w.rows, w.K
     y = _output(out, x.shape[:-1], N, index)
     if M:
-        ws, nbytes = _scratch(workspace, mx4_linear_workspace_bytes(M, N, K), index)
-        _check(lib().w8a8_mx4_linear(x2.data_ptr(), ldx, w.image.data_ptr(), _at(bias), y.data_ptr(), M, N,
-                                     K, act, _at(ws), nbytes, s), "w8a8_mx4_linear")
+        ws, nbytes = _scratch(workspace, 0 if M <= 16 else mx4_bytes(M, K), index)
+        _check(lib().w8a8_mx4_linear(x2.data_ptr(), ldx, w.image.data_ptr(), _at(bias), y.data_ptr(), M, N, K,
+                                     act, _at(ws), nbytes, _raw_stream(index)), "w8a8_mx4_linear")
     return y
 
 
@@ -224,20 +228,24 @@ def mx4_linear_quant(x: torch.Tensor, w: MX4Tensor, bias: Optional[torch.Tensor]
                      stream=None, act: int = ACT_NONE) -> MX4Tensor:
     """A layer whose output feeds another 4-bit layer: the image of y, equal to
     ``mx4_quant(mx4_linear(...))``."""
-    _need_cuda(x, "x", torch.bfloat16)
     _weight(w, bias, x.shape[-1])
+    return _linear_quant(x, w, bias, image, workspace, stream, act)
+
+
+def _linear_quant(x, w, bias, image, workspace, stream, act):
+    """``mx4_linear_quant`` with a weight and bias that have been checked."""
+    _need_cuda(x, "x", torch.bfloat16)
     index = _device(x, w.image, bias, image, workspace)
     if _elsewhere(index, stream):
         with _there(index, stream):
-            return mx4_linear_quant(x, w, bias, image, workspace, act=act)
-    s = _raw_stream(index)
+            return _linear_quant(x, w, bias, image, workspace, None, act)
     x2, M, ldx = _rows_of(x)
     N, K = w.rows, w.K
     y = _image(image, M, N, index)
     if M:
-        ws, nbytes = _scratch(workspace, mx4_linear_workspace_bytes(M, N, K), index)
+        ws, nbytes = _scratch(workspace, 0 if M <= 16 else mx4_bytes(M, K), index)
         _check(lib().w8a8_mx4_linear_quant(x2.data_ptr(), ldx, w.image.data_ptr(), _at(bias), y.data_ptr(),
-                                           y.numel(), M, N, K, act, _at(ws), nbytes, s),
+                                           y.numel(), M, N, K, act, _at(ws), nbytes, _raw_stream(index)),
                "w8a8_mx4_linear_quant")
     return MX4Tensor(y, x.shape[:-1], N)
 
@@ -263,13 +271,20 @@ class MX4Linear:
         self.w, self.act = w, act
         self.N, self.K = w.rows, w.K
         self.bias = None if bias is None else bias.to(device=w.device, dtype=torch.bfloat16).contiguous()
+        _weight(w, self.bias, self.K)
 
     def __call__(self, x, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """x: bf16 [..., K] or an MX4Tensor -> y bf16 [..., N]."""
-        f = mx4_scaled_mm if isinstance(x, MX4Tensor) else mx4_linear
-        return f(x, self.w, self.bias, out=out, stream=stream, act=self.act)
+        if isinstance(x, MX4Tensor):
+            return mx4_scaled_mm(x, self.w, self.bias, out=out, stream=stream, act=self.act)
+        if x.shape[-1] != self.K:
+            raise ValueError(f"x has K = {x.shape[-1]}, the weight K = {self.K}")
+        return _linear(x, self.w, self.bias, out, None, stream, self.act)
 
     def quantised(self, x, image: Optional[torch.Tensor] = None, stream=None) -> MX4Tensor:
         """The same output, in the form the next 4-bit layer takes."""
-        f = mx4_scaled_mm_quant if isinstance(x, MX4Tensor) else mx4_linear_quant
-        return f(x, self.w, self.bias, image=image, stream=stream, act=self.act)
+        if isinstance(x, MX4Tensor):
+            return mx4_scaled_mm_quant(x, self.w, self.bias, image=image, stream=stream, act=self.act)
+        if x.shape[-1] != self.K:
+            raise ValueError(f"x has K = {x.shape[-1]}, the weight K = {self.K}")
+        return _linear_quant(x, self.w, self.bias, image, None, stream, self.act)
