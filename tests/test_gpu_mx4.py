@@ -212,3 +212,22 @@ def test_product_of_many_rows_on_either_path(M, N, K, act, path):
                 assert (c[M:] == 255).all() and (s[M:] == 255).all()
     finally:
         w8.set_path(w8.PATH_AUTO)
+
+
+@pytest.mark.parametrize("M,N,K", [(13, 5120, 2064), (30, 5120, 2064), (60, 5120, 4112), (3, 12288, 4112),
+                                   (8, 20864, 7440), (20, 20864, 7440), (60, 20864, 7440), (1, 27648, 5120)])
+def test_product_of_few_rows_over_every_split(M, N, K):
+    """Clusters of one to four CTAs, one slab each or several in turn, against the 64-bit product of the values."""
+    g = torch.Generator(device="cuda").manual_seed(N + K)
+    x = torch.randn(M, K, device="cuda", generator=g).bfloat16()
+    w = w8.mx4_quant(torch.randn(N, K, device="cuda", generator=g).mul_(K ** -0.5).bfloat16())
+    b = torch.randn(N, device="cuda", generator=g).bfloat16()
+    a = w8.mx4_quant(x)
+    va, vw = a.dequant().double(), w.dequant().double()
+    t = va @ vw.t() + b.double()
+    err = (K / 64 + 8) * 2.0 ** -22 * (va.abs() @ vw.abs().t()) + 2.0 ** -23 * t.abs()
+    y = w8.mx4_scaled_mm(a, w, b)
+    assert ((y.double() - t).abs() <= err + HALF * (t.abs() + err)).all()
+    for _ in range(4):
+        assert torch.equal(w8.mx4_linear(x, w, b), y)
+    assert all(torch.equal(p, q) for p, q in zip(w8.mx4_linear_quant(x, w, b).unpack(), w8.mx4_quant(y).unpack()))

@@ -4,7 +4,10 @@ Dynamic per-token symmetric int8 activation quantisation, a load-time weight
 repack into tensor-core tile images, and int8 x int8 -> int32 GEMMs on the
 sm_100a tensor cores (tcgen05, TMEM accumulators) with a dequantising bf16
 epilogue -- exposed as the C ABI of libw8a8.so (include/w8a8.h) and bound here
-with ctypes.  The library is loaded on first use; there is no CPU fallback.
+with ctypes.  Beside them the same layers with both operands in microscaled
+4-bit (``MX4Linear``, ``mx4_*``), and the norms around a block with its gate and
+residual, which form the next layer's codes (``block_norm``).  The library is
+loaded on first use; there is no CPU fallback.
 """
 from .binding import (  # noqa: F401
     ACT_GELU_TANH, ACT_NONE, PATH_AUTO, PATH_LARGE, PATH_LARGE_BN128, PATH_LARGE_BN256, PATH_LARGE_PAIR, PATH_LARGE_PAIR128,

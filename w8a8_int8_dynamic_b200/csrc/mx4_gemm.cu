@@ -173,6 +173,7 @@ __global__ void __maxnreg__(kGemmRegs)
     // idle
   } else if (warp == 1) {
     // ---------------- MMA issuer: the warp waits, one elected lane issues ----
+    griddep_wait();  // the bounded waits below start when the data may come
     const bool lead = elect_one();
     const uint64_t a_desc0 = sw128_kmajor_desc(smem), sc_desc0 = mx4_scale_desc(smem);
     uint32_t s = 0, ph = 0;

@@ -181,6 +181,7 @@ __global__ void __maxnreg__(kGemmRegs)
     if (rank == 0) {
       // ---------------- MMA issuer (even CTA) ----------------
       // The whole warp walks the steps and waits; one elected lane issues.
+      griddep_wait();  // the bounded waits below start when the data may come
       const bool lead = elect_one();
       const uint64_t a_desc0 = sw128_kmajor_desc(smem), sc_desc0 = mx4_scale_desc(smem);
       const uint32_t sf0 = tmem_base + kScaleBase;

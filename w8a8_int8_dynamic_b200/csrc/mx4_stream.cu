@@ -210,6 +210,7 @@ __global__ void __launch_bounds__(kStreamThreads + (QUANT ? 32 * kQuantWarps : 0
     __syncwarp();
   } else if (warp == 1) {
     // ---------------- MMA issuer: the warp waits, one elected lane issues ----
+    griddep_wait();  // the bounded waits below start when the data may come
     const bool lead = elect_one();
     const uint64_t desc0 = sw128_kmajor_desc(smem), sc_desc0 = mx4_scale_desc(smem);
     uint32_t s = 0, ph = 0;

@@ -244,7 +244,7 @@ const char *w8a8_status_string(int status) {
   }
 }
 
-int w8a8_abi_version(void) { return (1 << 16) | 1; }
+int w8a8_abi_version(void) { return (1 << 16) | 2; }
 
 w8a8_status w8a8_set_path(int path) {
   if (path < 0 || path > 7 || path == 6) return W8A8_ERR_INVALID_ARG;
