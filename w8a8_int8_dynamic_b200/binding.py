@@ -527,18 +527,22 @@ class W8A8Linear:
         if _elsewhere(index, stream):
             with _there(index, stream):
                 return self.apply_codes(q, a_scale, out)
+        lead = q.shape[:-1]
         if out is None:
-            out = torch.empty((*q.shape[:-1], self.N), dtype=torch.bfloat16, device=index)
+            y = (torch.empty_strided((M, self.N), (self.N, 1), dtype=torch.bfloat16, device=index)
+                 if len(lead) == 1 else torch.empty((*lead, self.N), dtype=torch.bfloat16, device=index))
         elif out.dtype != torch.bfloat16 or out.numel() != M * self.N or not out.is_contiguous():
             raise ValueError(f"out must be contiguous bf16 and hold [{M}, {self.N}]")
+        else:
+            y = out.view(*lead, self.N)
         if M:
             need = _size("w8a8_scaled_mm_workspace_bytes", index, M, self.N, self.K)
             ws = _bytes(need, index) if need else None
             _check(lib().w8a8_scaled_mm_act(q.data_ptr(), a_scale.data_ptr(), self.packed.data_ptr(),
-                                            self.w_scale.data_ptr(), _at(self.bias), out.data_ptr(), M,
+                                            self.w_scale.data_ptr(), _at(self.bias), y.data_ptr(), M,
                                             self.N, self.K, self.act, _at(ws), need, _raw_stream(index)),
                    "w8a8_scaled_mm_act")
-        return out.view(*q.shape[:-1], self.N)
+        return y
 
     def split(self, y: torch.Tensor):
         return torch.split(y, list(self.splits), dim=-1)

@@ -53,6 +53,22 @@ def _vector(t: Optional[torch.Tensor], name: str, K: int) -> int:
     return t.data_ptr()
 
 
+def _per_group(t: torch.Tensor, name: str, K: int, groups: int):
+    """(t as [groups, K] with rows on 16-byte boundaries, its address, groups, row stride)."""
+    _need_cuda(t, name, torch.bfloat16)
+    if t.dim() == 1:
+        t = t.view(1, -1)
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != K or (groups and shape[0] != groups):
+        raise ValueError(f"{name} must be [groups, {K}], with as many groups as the others, got {list(shape)}")
+    groups = shape[0]
+    ld, step = t.stride()
+    if step != 1 or (groups > 1 and (ld % 8 or ld < K)):
+        t = t.contiguous()
+        ld = K
+    return t, t.data_ptr(), groups, ld if groups > 1 else K
+
+
 def block_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, *, post: Optional[Norm] = None,
                gate: Optional[torch.Tensor] = None, residual_scale: float = 1.0,
                pre: Optional[Norm] = None, scale: Optional[torch.Tensor] = None,
@@ -119,21 +135,17 @@ def block_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, *, post
             if M > 1:
                 ldro = n2.stride(0)
 
-    groups, held, places = 0, [], []
-    for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
-        if t is None:
-            places.append((0, 0))
-            continue
-        _need_cuda(t, name, torch.bfloat16)
-        if t.dim() == 1:
-            t = t.view(1, -1)
-        shape = t.shape
-        if len(shape) != 2 or shape[1] != K or (groups and shape[0] != groups):
-            raise ValueError(f"{name} must be [groups, {K}], with as many groups as the others, "
-                             f"got {list(shape)}")
-        t, groups, ld = _rows_of(t)
-        held.append(t)  # what a copy was made of, until the launch
-        places.append((t.data_ptr(), ld))
+    groups, held = 0, []
+    gate_at = scale_at = shift_at = ld_gate = ld_scale = ld_shift = 0
+    if gate is not None:
+        gate, gate_at, groups, ld_gate = _per_group(gate, "gate", K, groups)
+        held.append(gate)  # what a copy was made of, until the launch
+    if scale is not None:
+        scale, scale_at, groups, ld_scale = _per_group(scale, "scale", K, groups)
+        held.append(scale)
+    if shift is not None:
+        shift, shift_at, groups, ld_shift = _per_group(shift, "shift", K, groups)
+        held.append(shift)
     if group_index is not None:
         _need_cuda(group_index, "group_index", torch.int32)
         if group_index.numel() != M or not group_index.is_contiguous():
@@ -154,8 +166,7 @@ def block_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, *, post
         args = _ARGS.pack(
             M, K, x2.data_ptr(), ldx, 0 if r2 is None else r2.data_ptr(), 0 if new is None else new.data_ptr(),
             ldr, ldro, dtype, residual_scale, *_vectors(post, K), *_vectors(pre, K),
-            places[0][0], places[1][0], places[2][0], places[0][1], places[1][1], places[2][1],
-            groups, rows_per_group, 0 if group_index is None else group_index.data_ptr(),
+            gate_at, scale_at, shift_at, ld_gate, ld_scale, ld_shift, groups, rows_per_group, 0 if group_index is None else group_index.data_ptr(),
             0 if out is None else out.data_ptr(), K, 0 if q is None else q.data_ptr(),
             0 if a_scale is None else a_scale.data_ptr(), 0 if image is None else image.data_ptr(),
             0 if image is None else image.numel())
