@@ -207,3 +207,26 @@ def test_strides_and_leading_sizes():
     assert shaped.residual.shape == shaped.y.shape == shaped.q.shape == (2, 3, 4, 528)
     assert torch.equal(shaped.y.view(24, 528), want.y) and got.y.shape == (24, 528)
     assert w8.block_norm(x[:0], r[:0], pre=n, codes="mx4").residual.shape == (0, 528)
+
+
+def test_group_index_without_vectors_leaves_only_negative_rows():
+    M, K = 23, 272
+    x, r, (pw, _), (w, _), _ = tensors(17, M, K)
+    index = torch.arange(M, dtype=torch.int32, device="cuda") * 1000
+    index[4] = index[22] = -3
+    keep = [m for m in range(M) if m not in (4, 22)]
+    kw = dict(post=w8.Norm("rms", pw), pre=w8.Norm("rms", w))
+    want, stream = w8.block_norm(x, r, **kw), r.clone()
+    out = w8.block_norm(x, stream, residual_out=stream, group_index=index, **kw)
+    assert torch.equal(stream[keep], want.residual[keep]) and torch.equal(out.y[keep], want.y[keep])
+    assert torch.equal(stream[[4, 22]], r[[4, 22]])
+
+
+def test_no_groups_refused():
+    x, r, _, _, (gate, scale, shift) = tensors(19, 5, 272, 3)
+    index = torch.zeros(5, dtype=torch.int32, device="cuda")
+    n = w8.Norm("rms")
+    for kw in (dict(gate=gate[:0]), dict(gate=gate[:0], pre=n, scale=scale), dict(pre=n, shift=shift[:0])):
+        for i in (None, index):
+            with pytest.raises(ValueError, match="groups"):
+                w8.block_norm(x, r, group_index=i, **kw)

@@ -59,7 +59,7 @@ def _per_group(t: torch.Tensor, name: str, K: int, groups: int):
     if t.dim() == 1:
         t = t.view(1, -1)
     shape = t.shape
-    if len(shape) != 2 or shape[1] != K or (groups and shape[0] != groups):
+    if len(shape) != 2 or shape[1] != K or not shape[0] or (groups and shape[0] != groups):
         raise ValueError(f"{name} must be [groups, {K}], with as many groups as the others, got {list(shape)}")
     groups = shape[0]
     ld, step = t.stride()
@@ -85,7 +85,7 @@ def block_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, *, post
     for an update in place) or to a new tensor.
     gate, scale, shift: bf16 [groups, K] (slices of a wider tensor may be given as they are; [K]
     for one group).  The group of row m is ``group_index[m]`` (int32; a row whose index is
-    outside the groups is padding and is left alone), else m // ``rows_per_group`` (default: all
+    outside the groups, or negative where none of the three is given, is padding and is left alone), else m // ``rows_per_group`` (default: all
     rows in one group).
     codes: "int8" (``q`` and ``a_scale``, for ``W8A8Linear.apply_codes``) or "mx4" (an ``MX4Tensor``, for
     ``MX4Linear``), equal to the codes of the bf16 output; None: y itself.  ``y=True`` gives y beside codes.
@@ -150,7 +150,7 @@ def block_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, *, post
         _need_cuda(group_index, "group_index", torch.int32)
         if group_index.numel() != M or not group_index.is_contiguous():
             raise ValueError(f"group_index must be contiguous and hold {M} values")
-        groups = groups or 1
+        groups = groups or 0x7FFFFFFF
     if rows_per_group is None:
         rows_per_group = M or 1
 
