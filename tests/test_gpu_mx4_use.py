@@ -258,3 +258,41 @@ def test_offsets_past_32_bits():
     big = w8.block_norm(x, x.float(), pre=n, post=n, codes="int8", y=True)
     for name in ("residual", "y", "q", "a_scale"):
         assert torch.equal(getattr(big, name)[tail], getattr(small, name))
+
+
+@pytest.mark.parametrize("M", [1, 20, 200])
+def test_ends_of_the_range(M):
+    """Sums past bf16 become infinities of their sign, products down to fp32's subnormals keep their value, a weight
+    block with the NaN scale gives NaN in its column alone."""
+    top = 6 * 2.0 ** 125  # 3e38 saturates: its block's scale is 2^125
+    for xs, ws, want in ((3e38, 100.0, float("inf")), (3e38, -100.0, -float("inf")), (3e38, 1.0, top),
+                         (2.0 ** -120, 1.0, 2.0 ** -120), (2.0 ** -100, 2.0 ** -30, 2.0 ** -130), (2.0 ** -133, 2.0 ** 100, 0.0)):
+        x, w = (torch.zeros(n, 64, dtype=torch.bfloat16, device="cuda") for n in (M, 16))
+        x[:, 5], w[:, 5] = xs, ws
+        y = w8.mx4_linear(x, w8.mx4_quant(w))
+        assert (y.double() == want).all()
+    x, w, b = operands(M, M, 272, 528)
+    codes, scales = w.unpack()
+    y = w8.mx4_linear(x, w, b)
+    scales[7, 3] = 255
+    got = w8.mx4_linear(x, w8.mx4_pack(codes, scales), b)
+    rest = [n for n in range(272) if n != 7]
+    assert got[:, 7].isnan().all() and torch.equal(got[:, rest], y[:, rest])
+
+
+def test_one_row_without_leading_sizes():
+    x, w, b = operands(3, 1, 272, 528)
+    v = x[0]
+    assert torch.equal(w8.mx4_linear(v, w, b), w8.mx4_linear(x, w, b)[0])
+    assert torch.equal(w8.mx4_quant(v).dequant(), w8.mx4_quant(x).dequant()[0])
+    n = w8.Norm("layer")
+    out, want = w8.block_norm(v, v.float(), pre=n, codes="int8"), w8.block_norm(x, x.float(), pre=n, codes="int8")
+    assert torch.equal(out.residual, want.residual[0]) and torch.equal(out.q, want.q[0])
+    assert torch.equal(out.a_scale, want.a_scale)
+
+
+def test_pack_of_other_than_a_matrix_refused():
+    codes, scales = (torch.zeros(2, 16, n, dtype=torch.uint8, device="cuda") for n in (8, 1))
+    for c, s in ((codes, scales), (codes, scales[:, 0]), (codes[0, 0], scales[0, 0])):
+        with pytest.raises(ValueError):
+            w8.mx4_pack(c, s)

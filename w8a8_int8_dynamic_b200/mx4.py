@@ -114,6 +114,8 @@ def mx4_pack(codes: torch.Tensor, scales: torch.Tensor, image: Optional[torch.Te
     (uint8 [rows, ceil(K/32)]) -> image."""
     _need_cuda(codes, "codes", torch.uint8)
     _need_cuda(scales, "scales", torch.uint8)
+    if codes.dim() != 2:
+        raise ValueError(f"codes must be [rows, K/2], got {list(codes.shape)}")
     index = _device(codes, scales, image)
     rows, K = codes.shape[0], codes.shape[1] * 2
     if tuple(scales.shape) != (rows, (K + 31) // 32):
