@@ -171,6 +171,17 @@ def _bytes(n: int, index: int) -> torch.Tensor:
     return torch.empty_strided((n,), (1,), dtype=torch.uint8, device=index)
 
 
+def _new(lead, N: int, dtype: torch.dtype, index: int) -> torch.Tensor:
+    """A new [*lead, N] (1.5 us where torch.empty takes 2.4 to 3.2)."""
+    strides, n = [1], N
+    for size in lead[:0:-1]:
+        strides.append(n)
+        n *= size
+    if lead:
+        strides.append(n)
+    return torch.empty_strided((*lead, N), strides[::-1], dtype=dtype, device=index)
+
+
 @functools.lru_cache(maxsize=4096)
 def _size(name: str, device: int, *shape: int) -> int:
     out = _SZ()
@@ -529,8 +540,7 @@ class W8A8Linear:
                 return self.apply_codes(q, a_scale, out)
         lead = q.shape[:-1]
         if out is None:
-            y = (torch.empty_strided((M, self.N), (self.N, 1), dtype=torch.bfloat16, device=index)
-                 if len(lead) == 1 else torch.empty((*lead, self.N), dtype=torch.bfloat16, device=index))
+            y = _new(lead, self.N, torch.bfloat16, index)
         elif out.dtype != torch.bfloat16 or out.numel() != M * self.N or not out.is_contiguous():
             raise ValueError(f"out must be contiguous bf16 and hold [{M}, {self.N}]")
         else:

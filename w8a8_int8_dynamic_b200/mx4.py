@@ -12,7 +12,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from .binding import (ACT_NONE, _at, _bytes, _check, _device, _elsewhere, _need_cuda, _raw_stream, _rows_of,
+from .binding import (ACT_NONE, _at, _bytes, _check, _device, _elsewhere, _need_cuda, _new, _raw_stream, _rows_of,
                       _size, _there, lib)
 
 
@@ -58,9 +58,7 @@ def _image(image: Optional[torch.Tensor], rows: int, K: int, index: int) -> torc
 def _output(out: Optional[torch.Tensor], lead: Tuple[int, ...], N: int, index: int) -> torch.Tensor:
     """A new [*lead, N], or ``out`` seen as one."""
     if out is None:
-        if len(lead) == 1:
-            return torch.empty_strided((lead[0], N), (N, 1), dtype=torch.bfloat16, device=index)
-        return torch.empty((*lead, N), dtype=torch.bfloat16, device=index)
+        return _new(lead, N, torch.bfloat16, index)
     _need_cuda(out, "out", torch.bfloat16)
     if not out.is_contiguous():
         raise ValueError("out must be contiguous")

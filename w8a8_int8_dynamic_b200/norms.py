@@ -6,7 +6,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from .binding import _bytes, _check, _device, _elsewhere, _need_cuda, _raw_stream, _rows_of, _there, lib
+from .binding import _bytes, _check, _device, _elsewhere, _need_cuda, _new, _raw_stream, _rows_of, _there, lib
 from .mx4 import MX4Tensor, mx4_bytes
 
 _KINDS = {"rms": 1, "layer": 2}
@@ -126,7 +126,7 @@ def block_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, *, post
         r2, _, ldr = _rows_of(residual)
         dtype, ldro = _RESIDUAL[residual.dtype], K
         if residual_out is None:
-            new = torch.empty_like(r2) if r2 is residual else torch.empty(x.shape, dtype=r2.dtype, device=index)
+            new = torch.empty_like(r2) if r2 is residual else _new(x.shape[:-1], K, r2.dtype, index)
         else:  # written in place: a view, never a copy
             new = residual_out
             n2 = new.view(-1, K) if new.is_contiguous() else new
@@ -156,9 +156,9 @@ def block_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, *, post
 
     out = q = a_scale = image = None
     if want_y:
-        out = torch.empty_like(x) if plain else torch.empty(x.shape, dtype=torch.bfloat16, device=index)
+        out = torch.empty_like(x) if plain else _new(x.shape[:-1], K, torch.bfloat16, index)
     if codes == "int8":
-        q = torch.empty(x.shape, dtype=torch.int8, device=index)
+        q = torch.empty_like(x, dtype=torch.int8) if plain else _new(x.shape[:-1], K, torch.int8, index)
         a_scale = torch.empty_strided((M,), (1,), dtype=torch.float32, device=index)
     elif codes == "mx4":
         image = _bytes(mx4_bytes(M, K) if M else 0, index)
