@@ -117,6 +117,9 @@ __global__ void __launch_bounds__(kStreamThreads + (QUANT ? 32 * kQuantWarps : 0
   using L = StreamCfg<NT>;
   constexpr int S = L::kStages;
   constexpr uint32_t kIdesc = idesc_mx4(128, NT);
+  // A quantising warp has seen the MMAs of the stage's round before last end
+  // (its own last tile waited for later ones), which a barrier's parity needs.
+  static_assert(!QUANT || kQuantWarps <= S, "quantising warps and the ring");
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -166,25 +169,31 @@ __global__ void __launch_bounds__(kStreamThreads + (QUANT ? 32 * kQuantWarps : 0
   const int nseg = first < args.slabs ? (args.slabs - 1 - first) / step + 1 : 0;
   const int64_t total = (int64_t)nseg * nk;
 
+  auto wait_all = [&](uint64_t *bar, uint32_t parity) {  // by a whole warp
+    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, args.p.status)) != 0;
+  };
   if (warp == 0) {
-    if (lane == 0) {
-      // ---------------- producer ----------------
-      const uint64_t evict_first = policy_evict_first();
-      const size_t slab_bytes = (size_t)kt * kMxTileBytes;
-      const uint8_t *w0 = args.p.w + (size_t)first * slab_bytes + (size_t)k_begin * kMxTileBytes;
-      // before the wait: DRAM to L2 only, in the order of the copies
+    // ---------------- producer: the warp waits, one elected lane issues ----
+    const bool lead = elect_one();
+    const uint64_t evict_first = policy_evict_first();
+    const size_t slab_bytes = (size_t)kt * kMxTileBytes;
+    const uint8_t *w0 = args.p.w + (size_t)first * slab_bytes + (size_t)k_begin * kMxTileBytes;
+    // before the wait: DRAM to L2 only, in the order of the copies
+    if (lead)
       for (int64_t i = 0, left = kPrefetchTiles; i < nseg && left > 0; ++i, left -= nk)
         bulk_prefetch_l2(w0 + (size_t)i * step * slab_bytes,
                          (uint32_t)(min((int64_t)nk, left) * kMxTileBytes));
-      griddep_wait();
-      uint32_t s = 0, ph = 0;
-      int64_t issued = 0;
-      bool ok = true;
-      for (int i = 0; ok && i < nseg; ++i) {
-        const uint8_t *w = w0 + (size_t)i * step * slab_bytes;
-        for (int k = 0; k < nk; ++k, ++issued) {
-          ok = issued < S || mbar_wait(&empty[s], ph ^ 1, abort_flag, args.p.status);
-          if (!ok) break;
+    __syncwarp();
+    griddep_wait();
+    uint32_t s = 0, ph = 0;
+    int64_t issued = 0;
+    bool ok = true;
+    for (int i = 0; ok && i < nseg; ++i) {
+      const uint8_t *w = w0 + (size_t)i * step * slab_bytes;
+      for (int k = 0; k < nk; ++k, ++issued) {
+        ok = issued < S || wait_all(&empty[s], ph ^ 1);
+        if (!ok) break;
+        if (lead) {
           uint8_t *st = smem + s * L::kStageBytes;
           mbar_arrive_expect_tx(&full[s], kMxTileBytes + (QUANT ? 0 : NT * 128 + kMxScaleBytes));
           bulk_load_hint(st, w + (size_t)k * kMxTileBytes, kMxTileBytes, &full[s], evict_first);
@@ -193,20 +202,22 @@ __global__ void __launch_bounds__(kStreamThreads + (QUANT ? 32 * kQuantWarps : 0
             bulk_load(st + L::kQ, t, NT * 128, &full[s]);
             bulk_load(st + L::kS, t + kMxCodeBytes, kMxScaleBytes, &full[s]);
           }
-          if (++s == (uint32_t)S) {
-            s = 0;
-            ph ^= 1;
-          }
+        }
+        __syncwarp();
+        if (++s == (uint32_t)S) {
+          s = 0;
+          ph ^= 1;
         }
       }
-      // Every copy issued lands before the CTA leaves, whatever gave up.  (With
-      // QUANT a stage whose codes never came stays incomplete: bounded too.)
+    }
+    // Every copy issued lands before the CTA leaves, whatever gave up.  (With
+    // QUANT a stage whose codes never came stays incomplete: bounded too.)
+    if (lead)
       for (int64_t sl = 0; sl < S && sl < issued; ++sl) {
         const int64_t last = sl + ((issued - 1 - sl) / S) * S;
         volatile int no_abort = 0;
         (void)mbar_wait_bounded(&full[sl], (uint32_t)((last / S) & 1), &no_abort, args.p.status);
       }
-    }
     __syncwarp();
   } else if (warp == 1) {
     // ---------------- MMA issuer: the warp waits, one elected lane issues ----
@@ -215,16 +226,13 @@ __global__ void __launch_bounds__(kStreamThreads + (QUANT ? 32 * kQuantWarps : 0
     const uint64_t desc0 = sw128_kmajor_desc(smem), sc_desc0 = mx4_scale_desc(smem);
     uint32_t s = 0, ph = 0;
     bool ok = true;
-    auto wait = [&](uint64_t *bar, uint32_t parity) {
-      return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, args.p.status)) != 0;
-    };
     for (int i = 0; ok && i < nseg; ++i) {
       const uint32_t b = i & 1, bph = (i >> 1) & 1;
-      ok = wait(&tempty[b], bph ^ 1);
+      ok = wait_all(&tempty[b], bph ^ 1);
       if (!ok) break;
       const uint32_t d_tmem = tmem_base + b * NT;
       for (int k = 0; k < nk; ++k) {
-        ok = wait(&full[s], ph);
+        ok = wait_all(&full[s], ph);
         if (!ok) break;
         tc_fence_after();
         if (lead) {
@@ -271,22 +279,19 @@ __global__ void __launch_bounds__(kStreamThreads + (QUANT ? 32 * kQuantWarps : 0
     float *parts = reinterpret_cast<float *>(smem + L::kRecv) + n_local;
     const uint32_t parts_addr = smem_addr(parts);
     const uint32_t recv_addr = smem_addr(recv), sent_addr = smem_addr(sent);
-    auto wait = [&](uint64_t *bar, uint32_t parity) {
-      return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, args.p.status)) != 0;
-    };
     for (int i = 0; i < nseg; ++i) {
       const int nb = first + i * step;
       const uint32_t b = i & 1, bph = (i >> 1) & 1;
       const int n = nb * 128 + n_local;
       const float bv =
           (args.p.bias && n < N) ? __uint_as_float((uint32_t)__ldg(args.p.bias + n) << 16) : 0.0f;
-      if (!wait(&tfull[b], bph)) break;
+      if (!wait_all(&tfull[b], bph)) break;
       tc_fence_after();
       const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + b * NT;
       // the parts that other CTAs finish go to them
       if (C > 1) {
         // (they have read the previous ones)
-        if (i > 0 && !(wait(sent, (uint32_t)(i - 1) & 1) && acquire_cluster(sent, (uint32_t)(i - 1) & 1))) break;
+        if (i > 0 && !(wait_all(sent, (uint32_t)(i - 1) & 1) && acquire_cluster(sent, (uint32_t)(i - 1) & 1))) break;
         for (int q = 0; q < chunks; ++q) {
           const int to = q % C;
           if (to == rank) continue;
@@ -302,7 +307,7 @@ __global__ void __launch_bounds__(kStreamThreads + (QUANT ? 32 * kQuantWarps : 0
         fence_cluster();
         __syncwarp();
         if (lane < C && lane != rank) arrive_release_cluster(map_to_cta(recv_addr, (uint32_t)lane));
-        if (!(wait(recv, (uint32_t)i & 1) && acquire_cluster(recv, (uint32_t)i & 1))) break;
+        if (!(wait_all(recv, (uint32_t)i & 1) && acquire_cluster(recv, (uint32_t)i & 1))) break;
       }
       // Few rows: a short loop, since this code runs once a slab and unrolled
       // over all 16 rows its instructions take longer to fetch than to execute
@@ -382,7 +387,7 @@ __global__ void __launch_bounds__(kStreamThreads + (QUANT ? 32 * kQuantWarps : 0
               v[j][g] = *reinterpret_cast<const uint4 *>(args.x + (int64_t)row * args.ldx + col + g * 8);
           }
         if (i >= S) {  // the stage's previous MMAs are done
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait(&empty[s], ph ^ 1, abort_flag, args.p.status)) != 0;
+          ok = wait_all(&empty[s], ph ^ 1);
           if (!ok) break;
         }
 #pragma unroll
