@@ -63,7 +63,12 @@ struct StreamArgs {
 constexpr double kDramBytesPerUs = 6.5e6, kSmBytesPerUs = 8e4, kJoinUs = 1.0;
 
 constexpr int kMaxCluster = 4;
-constexpr int kPrefetchTiles = 16;  // 272 KB a CTA, 40 MB in all
+// A CTA's weight tiles asked into L2 before the wait for the preceding kernel:
+// half of its own, at most 16 (40 MB in all).  More take DRAM time from that
+// kernel's own last reads, fewer leave DRAM idle in the change (1 row, product
+// on codes: 8192 x 8192, all / half / 4 tiles 10.2, 9.6, 9.8 us; 27648 x 5120,
+// at most 16 / 8 / 4 tiles 12.6, 13.0, 14.1).
+constexpr int kPrefetchTiles = 16;
 constexpr int kStreamThreads = 192;
 constexpr int kQuantWarps = 8;
 
@@ -180,7 +185,7 @@ __global__ void __launch_bounds__(kStreamThreads + (QUANT ? 32 * kQuantWarps : 0
     const uint8_t *w0 = args.p.w + (size_t)first * slab_bytes + (size_t)k_begin * kMxTileBytes;
     // before the wait: DRAM to L2 only, in the order of the copies
     if (lead)
-      for (int64_t i = 0, left = kPrefetchTiles; i < nseg && left > 0; ++i, left -= nk)
+      for (int64_t i = 0, left = min((int64_t)kPrefetchTiles, (total + 1) / 2); i < nseg && left > 0; ++i, left -= nk)
         bulk_prefetch_l2(w0 + (size_t)i * step * slab_bytes,
                          (uint32_t)(min((int64_t)nk, left) * kMxTileBytes));
     __syncwarp();
