@@ -337,18 +337,18 @@ __global__ void __maxnreg__(REGS) block_norm_kernel(const __grid_constant__ Norm
       group = (int)(row / a.rows_per_group);
       run = (int)min((int64_t)end, (group + 1) * a.rows_per_group);
     }
+    auto load = [&](int i, Raw<CPL, RES> &d) {
+      fetch<CPL, RES>(reinterpret_cast<const uint8_t *>(a.x + i * a.ldx + at.c0 * 8),
+                      static_cast<const uint8_t *>(a.residual) + (i * a.ldr + at.c0 * 8) * kRes, at, d);
+    };
+    Raw<CPL, RES> next;
+    load(row, next);  // in flight while the vectors are folded
     if (a.folded && group != have) {
       __syncthreads();
       fold(a, folded, group);
       __syncthreads();
       have = group;
     }
-    auto load = [&](int i, Raw<CPL, RES> &d) {
-      fetch<CPL, RES>(reinterpret_cast<const uint8_t *>(a.x + i * a.ldx + at.c0 * 8),
-                      static_cast<const uint8_t *>(a.residual) + (i * a.ldr + at.c0 * 8) * kRes, at, d);
-    };
-    Raw<CPL, RES> next;
-    load(row, next);
     for (; row < run; ++row) {
       const Raw<CPL, RES> cur = next;
       if (row + 1 < run) load(row + 1, next);
