@@ -174,7 +174,7 @@ def test_group_index_and_padding_rows():
     assert torch.equal(c[keep], cw[keep]) and torch.equal(s[keep], sw[keep])
 
 
-@pytest.mark.parametrize("M,K", [(1500, 264), (700, 1040), (400, 4104)])
+@pytest.mark.parametrize("M,K", [(1500, 264), (700, 1040), (400, 4104), (350, 10248), (350, 12304)])
 def test_many_rows_with_a_group_and_padding_each(M, K):
     """Several rows a CTA, groups that change and recur, padding rows between them, one norm or both."""
     groups = 7

@@ -495,14 +495,14 @@ __global__ void __maxnreg__(REGS) block_norm_kernel(const __grid_constant__ Norm
   }
 }
 
-FuncAttrOnce g_norm_attr[3][3];            // [shape of the instance][residual]
+FuncAttrOnce g_norm_attr[4][3];            // [shape of the instance][residual]
 constexpr int kMaxFolded = 4 * 4 * 14336;  // shared memory that a launch may ask for: 224 KB
 
 template <int CPL, int RES, int REGS>
 cudaError_t run(const cudaLaunchConfig_t &cfg, const NormArgs &a) {
   auto k = block_norm_kernel<CPL, RES, REGS>;
   if (cfg.dynamicSmemBytes > 40000) {
-    const cudaError_t e = g_norm_attr[CPL == 2 ? 0 : REGS == 128 ? 1 : 2][RES].ensure(
+    const cudaError_t e = g_norm_attr[REGS == 160 ? 3 : CPL - 2][RES].ensure(
         [&] { return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxFolded); });
     if (e != cudaSuccess) return e;
   }
@@ -600,9 +600,10 @@ extern "C" w8a8_status w8a8_block_norm(const w8a8_block_norm_args *p, w8a8_strea
   // from its elements is then as much as on them, but a row is soon done.
   // Four (160 registers) for many rows a CTA with a bf16 residual: 8192 x 4096
   // with both norms 59 us, with two chunks 68; but 2048 x 4096 26 and 23, and
-  // with an fp32 residual 79 and 75.  Four (128 registers) where two would
-  // need more than 16 warps.  An image's padding columns count (the lanes that
-  // hold them write them).
+  // with an fp32 residual 79 and 75.  Three, then four (128 registers), where
+  // two would need more than 16 warps: 4000 x 10240 with both norms and an fp32
+  // residual 116 us with three, 175 with four.  An image's padding columns
+  // count (the lanes that hold them write them).
   const int64_t nchunks = a.image ? (int64_t)a.kt * 32 : K / 8;
   int cpl = 2, regs = 128;
   int64_t resident = 0, smem = 0;
@@ -617,8 +618,10 @@ extern "C" w8a8_status w8a8_block_norm(const w8a8_block_norm_args *p, w8a8_strea
     resident = sm_count() * std::min<int64_t>(32, std::max<int64_t>(1, fit));
   };
   shape(4, 160);
-  if (nchunks > kMaxWarps * 64)
+  if (nchunks > kMaxWarps * 96)
     shape(4, 128);
+  else if (nchunks > kMaxWarps * 64)
+    shape(3, 128);
   else if (a.residual_f32 || M < 8 * resident)
     shape(2, 128);
   if (smem > kMaxFolded) return W8A8_ERR_UNSUPPORTED_SHAPE;
@@ -632,7 +635,10 @@ extern "C" w8a8_status w8a8_block_norm(const w8a8_block_norm_args *p, w8a8_strea
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cpl == 2 ? run<2, 128>(cfg, a) : regs == 128 ? run<4, 128>(cfg, a) : run<4, 160>(cfg, a);
+  const cudaError_t e = cpl == 2      ? run<2, 128>(cfg, a)
+                        : cpl == 3    ? run<3, 128>(cfg, a)
+                        : regs == 128 ? run<4, 128>(cfg, a)
+                                      : run<4, 160>(cfg, a);
   if (e == cudaSuccess) count_launch();
   return from_cuda(e);
 }
