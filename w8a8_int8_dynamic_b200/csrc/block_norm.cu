@@ -596,14 +596,18 @@ extern "C" w8a8_status w8a8_block_norm(const w8a8_block_norm_args *p, w8a8_strea
 
   a.folded = ((a.gate || a.post_w) ? kFoldBranch : 0) | (a.post_b ? kFoldBranchAdd : 0) |
              ((a.pre_w || a.scale) ? kFoldMul : 0) | ((a.pre_b || a.shift) ? kFoldAdd : 0);
-  // Chunks per lane.  Two (128 registers): what a warp spends on a row apart
-  // from its elements is then as much as on them, but a row is soon done.
-  // Four (160 registers) for many rows a CTA with a bf16 residual: 8192 x 4096
-  // with both norms 59 us, with two chunks 68; but 2048 x 4096 26 and 23, and
-  // with an fp32 residual 79 and 75.  Three, then four (128 registers), where
-  // two would need more than 16 warps: 4000 x 10240 with both norms and an fp32
-  // residual 116 us with three, 175 with four.  An image's padding columns
-  // count (the lanes that hold them write them).
+  // Chunks per lane: two, three or four, so that a CTA has at most 16 warps.
+  // Where a choice is left, by the warps that an SM then holds (a row's CTA
+  // may not fit twice).  Three if that makes a quarter more warps than two:
+  // both norms, 4096 x 5120 60 us with two (10 warps), 45 with three (14);
+  // but 4096 x 7168 67 with two (14), 76 with three (10).  Four with 160
+  // registers for many rows a CTA, without an fp32 residual or an image, if at
+  // most a quarter of the warps is lost: a row takes longer, but fewer
+  // instructions (8192 x 4096 59 us, with two chunks 67; 1000 x 4096 13.9 and
+  // 13.0; 4096 x 4096 with an fp32 residual 44.1 and 43.1; to 4-bit codes 31.4
+  // and 30.4; 4096 x 8192, half the warps, 77 and 68).  Past 8192 three, where
+  // they suffice (4000 x 10240, fp32 residual, 116 us; with four 175).  An
+  // image's padding columns count (the lanes that hold them write them).
   const int64_t nchunks = a.image ? (int64_t)a.kt * 32 : K / 8;
   int cpl = 2, regs = 128;
   int64_t resident = 0, smem = 0;
@@ -617,13 +621,21 @@ extern "C" w8a8_status w8a8_block_norm(const w8a8_block_norm_args *p, w8a8_strea
     const int64_t fit = std::min<int64_t>(65536 / r / (32 * a.W), (int64_t)226 * 1024 / (smem + 2048));
     resident = sm_count() * std::min<int64_t>(32, std::max<int64_t>(1, fit));
   };
-  shape(4, 160);
-  if (nchunks > kMaxWarps * 96)
+  auto warps = [&](int c, int r) {
+    shape(c, r);
+    return resident * a.W;
+  };
+  if (nchunks > kMaxWarps * 96) {
     shape(4, 128);
-  else if (nchunks > kMaxWarps * 64)
+  } else if (nchunks > kMaxWarps * 64) {
     shape(3, 128);
-  else if (a.residual_f32 || M < 8 * resident)
-    shape(2, 128);
+  } else {
+    const int64_t three = warps(3, 128), two = warps(2, 128);
+    const int c = three * 4 > two * 5 ? 3 : 2;
+    const bool four = !a.residual_f32 && !a.image && warps(4, 160) * 4 >= (c == 3 ? three : two) * 3 &&
+                      M >= 8 * resident;
+    if (!four) shape(c, 128);
+  }
   if (smem > kMaxFolded) return W8A8_ERR_UNSUPPORTED_SHAPE;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)std::min(M, resident));
