@@ -427,7 +427,7 @@ w8a8_status w8a8_block_norm(const w8a8_block_norm_args *args, w8a8_stream_t stre
  * 2-SM GEMM with 256 x 128 tiles.  6 (and anything above 7) is not a path:
  * W8A8_ERR_INVALID_ARG.  Each path is also chosen automatically, by shape.
  * For the 4-bit products 1, 3 and 4 are the 1-SM kernel, 2 the weight-streaming
- * one (M <= 64 only), 5 and 7 the CTA-pair one; a 4-bit layer of at most 16
+ * one (M <= 128 only), 5 and 7 the CTA-pair one; a 4-bit layer of at most 16
  * rows always streams the weights.
  * Process-wide; not synchronised with concurrent calls. */
 w8a8_status w8a8_set_path(int path);

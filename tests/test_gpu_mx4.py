@@ -162,7 +162,8 @@ def test_product_with_codes_of_its_output(M, N, K, act):
 @pytest.mark.parametrize("path", [w8.PATH_LARGE, w8.PATH_SMALL])
 @pytest.mark.parametrize("M,N,K", [(1, 1000, 5120), (4, 520, 13824), (16, 4096, 1040), (16, 136, 8208), (13, 5120, 784),
                                    (17, 4096, 528), (30, 136, 13824), (64, 2056, 4112), (50, 8, 16384),
-                                   (33, 27648, 272)])
+                                   (33, 27648, 272), (65, 1000, 5136), (100, 4096, 528), (128, 136, 13824),
+                                   (77, 27648, 272)])
 def test_product_of_few_rows_on_either_path(M, N, K, path):
     """One and several slabs a cluster, K whole and split in up to eight: both kernels, y and its codes."""
     x, w, b = operands(M + N + K, M, N, K)
@@ -215,7 +216,8 @@ def test_product_of_many_rows_on_either_path(M, N, K, act, path):
 
 
 @pytest.mark.parametrize("M,N,K", [(13, 5120, 2064), (30, 5120, 2064), (60, 5120, 4112), (3, 12288, 4112),
-                                   (8, 20864, 7440), (20, 20864, 7440), (60, 20864, 7440), (1, 27648, 5120)])
+                                   (8, 20864, 7440), (20, 20864, 7440), (60, 20864, 7440), (1, 27648, 5120),
+                                   (65, 5120, 7440), (97, 1040, 13824), (128, 6152, 12304), (128, 5120, 5136)])
 def test_product_of_few_rows_over_every_split(M, N, K):
     """Clusters of one to four CTAs, one slab each or several in turn, against the 64-bit product of the values."""
     g = torch.Generator(device="cuda").manual_seed(N + K)
@@ -230,4 +232,5 @@ def test_product_of_few_rows_over_every_split(M, N, K):
     assert ((y.double() - t).abs() <= err + HALF * (t.abs() + err)).all()
     for _ in range(4):
         assert torch.equal(w8.mx4_linear(x, w, b), y)
-    assert all(torch.equal(p, q) for p, q in zip(w8.mx4_linear_quant(x, w, b).unpack(), w8.mx4_quant(y).unpack()))
+    if N % 16 == 0:  # an output image's condition
+        assert all(torch.equal(p, q) for p, q in zip(w8.mx4_linear_quant(x, w, b).unpack(), w8.mx4_quant(y).unpack()))

@@ -213,7 +213,8 @@ struct Mx4Args {
 
 // Few rows (mx4_stream.cu), M <= kStreamRows.  x: bf16 rows that the kernel
 // quantises itself (M <= kStreamQuantRows), or null: p.a is their image.
-constexpr int64_t kStreamRows = 64, kStreamQuantRows = 16;
+constexpr int64_t kStreamRows = 128, kStreamQuantRows = 16;
+constexpr int kMaxStreamCluster = 4;
 w8a8_status launch_mx4_stream(const Mx4Args &p, const void *x, int64_t ldx, int64_t K, cudaStream_t stream);
 
 // Many rows (mx4_pair.cu): 256 x 256 tiles on CTA pairs.

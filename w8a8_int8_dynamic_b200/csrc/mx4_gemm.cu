@@ -330,10 +330,17 @@ w8a8_status launch_mx4_1sm(const CUtensorMap &ty, Mx4Args a, cudaStream_t stream
   return from_cuda(e);
 }
 
-// Up to 64 rows the weight stream sets the time (mx4_stream.cu).
-bool use_stream(int64_t M) {
+// Up to 64 rows the weight stream sets the time (mx4_stream.cu).  Up to 128 it
+// is worth its longer end where clusters that split K save 18 steps of it or
+// more (us, stream and single CTAs, 128 rows: N = 5120, K = 13824 15.1, 18.3;
+// 1024, 8192 8.6, 11.9; 2048, 6144, which saves 18, 8.2, 9.9; 8192, 8192, 16,
+// 14.0, 13.5; 5120, 5120, 13, 10.9, 10.0).
+bool use_stream(const Mx4Args &a) {
   const int p = forced_path();
-  return M <= kStreamRows && (p == 0 || p == 2);
+  if (p != 0 || a.M > kStreamRows) return p == 2;
+  if (a.M <= 64) return true;
+  const int C = (int)std::min<int64_t>(kMaxStreamCluster, sm_count() / mx4_slabs(a.N));
+  return C > 1 && a.kt - (a.kt + C - 1) / C >= 18;
 }
 
 // Pairs with 256 x 256 tiles or single CTAs with 128 x 128 ones: by the rounds
@@ -373,7 +380,7 @@ w8a8_status launch_mx4(const void *a_image, const void *w_image, const void *bia
   a.status = status_word();
   if (!a.status) return W8A8_ERR_CUDA;
   if (forced_path() == 2 && M > kStreamRows) return W8A8_ERR_INVALID_ARG;
-  if (x || use_stream(M)) return launch_mx4_stream(a, x, ldx, K, stream);
+  if (x || use_stream(a)) return launch_mx4_stream(a, x, ldx, K, stream);
   if (use_pair(a)) return launch_mx4_pair(a, stream);
   CUtensorMap ty = {};
   if (y && !make_tmap_out_bf16(&ty, y, (uint64_t)M, (uint64_t)N)) return W8A8_ERR_CUDA;

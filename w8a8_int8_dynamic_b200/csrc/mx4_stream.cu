@@ -1,10 +1,13 @@
 // mx4_stream.cu -- the 4-bit product for few rows: every SM streams its share
 // of the weights.
 //
-// With M <= 64 rows the weights are most of the bytes, so they set the time.
+// With few rows (M <= 64, and to 128 where K is long and there are few slabs)
+// the weights are most of the bytes, so they set the time.
 // Swap-AB: a 128-row weight tile is the MMA's M operand and the rows of x (16,
-// 32 or 64 of them) its N operand.  A pipeline stage is one weight tile (17 KB,
-// one copy, codes and scales) and the rows' codes of the same 256 elements.
+// 32, 64 or 128 of them) its N operand.  A pipeline stage is one weight tile
+// (17 KB, one copy, codes and scales) and the rows' codes of the same 256
+// elements.  From 64 rows on the epilogue has two sets of four warps, which
+// take the chunks of 16 rows in turn (128 x 27648 x 5120 26.1 us, now 20.8).
 //
 // Work split: a cluster of C CTAs (1 to 4) takes a 128-row weight slab,
 // each CTA a C-th of its K; clusters are persistent over the slabs.  The
@@ -35,18 +38,21 @@ namespace {
 
 template <int NT>
 struct StreamCfg {
-  static constexpr int kStages = NT == 16 ? 9 : NT == 32 ? 8 : 7;
+  static constexpr int kStages = NT == 16 ? 9 : NT == 32 ? 8 : NT == 64 ? 7 : 4;
+  static constexpr int kSets = NT >= 64 ? 2 : 1;  // of four epilogue warps
+  static constexpr int kThreads = 64 + 128 * kSets;
   static constexpr int kQ = kMxTileBytes;             // codes of NT rows of x
   static constexpr int kS = kQ + NT * 128;            // their scales
   static constexpr int kStageBytes = kS + kMxScaleBytes;  // a multiple of 1024
   static constexpr int kRecv = kStages * kStageBytes;  // the parts of the cluster's CTAs
-  static constexpr int kBars = kRecv + 4 * 16 * 128 * 4;  // C * ceil(NT / 16 / C) chunks: at most 4
+  static constexpr int kChunks = NT == 128 ? 9 : 4;  // C * ceil(NT / 16 / C) of them at most
+  static constexpr int kBars = kRecv + kChunks * 16 * 128 * 4;
   // full[S], empty[S], tfull[2], tempty[2], recv, sent, done
   static constexpr int kMisc = kBars + (2 * kStages + 7) * 8;
   static constexpr int kAlloc = kMisc + 16 + 1024;
   // TMEM: two accumulators of NT columns, then each stage's scale columns
-  static constexpr uint32_t kTmemCols = 256;
-  static_assert(kStageBytes % 1024 == 0 && kAlloc <= 232448 && 2 * NT + kStages * 16 <= 256,
+  static constexpr uint32_t kTmemCols = NT == 128 ? 512 : 256;
+  static_assert(kStageBytes % 1024 == 0 && kAlloc <= 232448 && 2 * NT + kStages * 16 <= (int)kTmemCols,
                 "one CTA's shared memory and TMEM");
 };
 
@@ -62,14 +68,12 @@ struct StreamArgs {
 // Bytes a microsecond that DRAM delivers, and that one SM's copies do.
 constexpr double kDramBytesPerUs = 6.5e6, kSmBytesPerUs = 8e4, kJoinUs = 1.0;
 
-constexpr int kMaxCluster = 4;
 // A CTA's weight tiles asked into L2 before the wait for the preceding kernel:
 // half of its own, at most 16 (40 MB in all).  More take DRAM time from that
 // kernel's own last reads, fewer leave DRAM idle in the change (1 row, product
 // on codes: 8192 x 8192, all / half / 4 tiles 10.2, 9.6, 9.8 us; 27648 x 5120,
 // at most 16 / 8 / 4 tiles 12.6, 13.0, 14.1).
 constexpr int kPrefetchTiles = 16;
-constexpr int kStreamThreads = 192;
 constexpr int kQuantWarps = 8;
 
 // ---- distributed shared memory -------------------------------------------------
@@ -117,7 +121,7 @@ __device__ __noinline__ void image_row(const Mx4Args &p, int row, int nb, int qu
 }
 
 template <int NT, bool QUANT>
-__global__ void __launch_bounds__(kStreamThreads + (QUANT ? 32 * kQuantWarps : 0), 1)
+__global__ void __launch_bounds__(StreamCfg<NT>::kThreads + (QUANT ? 32 * kQuantWarps : 0), 1)
     mx4_stream_kernel(const StreamArgs args) {
   using L = StreamCfg<NT>;
   constexpr int S = L::kStages;
@@ -150,10 +154,10 @@ __global__ void __launch_bounds__(kStreamThreads + (QUANT ? 32 * kQuantWarps : 0
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 4);
+      mbar_init(&tempty[b], 4 * L::kSets);
     }
-    mbar_init(recv, 4 * (C > 1 ? C - 1 : 1));
-    mbar_init(sent, 4 * (C > 1 ? C - 1 : 1));
+    mbar_init(recv, 4 * L::kSets * (C > 1 ? C - 1 : 1));
+    mbar_init(sent, 4 * L::kSets * (C > 1 ? C - 1 : 1));
     mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -272,10 +276,10 @@ __global__ void __launch_bounds__(kStreamThreads + (QUANT ? 32 * kQuantWarps : 0
       (void)mbar_wait_bounded(mma_done, 0, &no_abort, args.p.status);
     }
     __syncwarp();
-  } else if (warp < 6) {
-    // ---------------- epilogue (warps 2..5): one output column per thread ----
+  } else if (warp < L::kThreads / 32) {
+    // ---- epilogue (one or two sets of four warps): one output column per thread ----
     griddep_wait();
-    const int quarter = warp & 3;
+    const int quarter = warp & 3, set = (warp - 2) >> 2;
     const int n_local = quarter * 32 + lane;
     const int M = args.p.M, N = args.p.N;
     // 16 rows of x a chunk; chunk q is finished by the CTA of rank q % C
@@ -297,7 +301,7 @@ __global__ void __launch_bounds__(kStreamThreads + (QUANT ? 32 * kQuantWarps : 0
       if (C > 1) {
         // (they have read the previous ones)
         if (i > 0 && !(wait_all(sent, (uint32_t)(i - 1) & 1) && acquire_cluster(sent, (uint32_t)(i - 1) & 1))) break;
-        for (int q = 0; q < chunks; ++q) {
+        for (int q = set; q < chunks; q += L::kSets) {
           const int to = q % C;
           if (to == rank) continue;
           uint32_t v[16];
@@ -319,9 +323,9 @@ __global__ void __launch_bounds__(kStreamThreads + (QUANT ? 32 * kQuantWarps : 0
       // (1 x 4096 x 4096: 7.3 us, four rows at a time 6.5).  With more rows the
       // latencies of a short loop cost more (64 x 27648 x 5120: two rows at a
       // time 22.7 us, eight 20.0, sixteen 18.2).
-      for (int q = rank; q < chunks; q += C) {
+      for (int q = rank + set * C; q < chunks; q += L::kSets * C) {
         const int m0 = q * 16, rows = min(16, M - m0);
-        float *part = parts + (C > 1 ? q / C * C : 0) * (16 * 128);
+        float *part = parts + (C > 1 ? q / C * C : set) * (16 * 128);
         {
           uint32_t v[16];
           tmem_ld_32x32b_x16(taddr + m0, v);
@@ -372,7 +376,7 @@ __global__ void __launch_bounds__(kStreamThreads + (QUANT ? 32 * kQuantWarps : 0
     // A lane takes block lane & 7 of every fourth row, all its loads in flight
     // together; a warp has the time of eight stages for its one.
     griddep_wait();
-    const int qw = warp - kStreamThreads / 32;
+    const int qw = warp - L::kThreads / 32;
     const int M = args.p.M, blk = lane & 7;
     uint32_t s = 0, ph = 0;  // the ring's first round needs no wait
     bool ok = true;
@@ -427,11 +431,11 @@ __global__ void __launch_bounds__(kStreamThreads + (QUANT ? 32 * kQuantWarps : 0
   }
 }
 
-FuncAttrOnce g_stream_attr[4];
+FuncAttrOnce g_stream_attr[5];
 
 template <int NT, bool QUANT>
 cudaError_t allow_smem() {
-  return g_stream_attr[QUANT ? 0 : NT == 16 ? 1 : NT == 32 ? 2 : 3].ensure([] {
+  return g_stream_attr[QUANT ? 0 : NT == 16 ? 1 : NT == 32 ? 2 : NT == 64 ? 3 : 4].ensure([] {
     return cudaFuncSetAttribute(mx4_stream_kernel<NT, QUANT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 StreamCfg<NT>::kAlloc);
   });
@@ -443,14 +447,14 @@ cudaError_t allow_smem() {
 template <int NT>
 int max_clusters(int C) {
   constexpr int kDevices = 64;
-  static std::atomic<int> known[kDevices][kMaxCluster + 1];  // + 1
+  static std::atomic<int> known[kDevices][kMaxStreamCluster + 1];  // + 1
   const int dev = current_device();
   const bool keep = dev >= 0 && dev < kDevices;
   int n = keep ? known[dev][C].load(std::memory_order_relaxed) - 1 : -1;
   if (n >= 0) return n;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)C);
-  cfg.blockDim = dim3(kStreamThreads);
+  cfg.blockDim = dim3(StreamCfg<NT>::kThreads);
   cfg.dynamicSmemBytes = StreamCfg<NT>::kAlloc;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -476,9 +480,9 @@ w8a8_status run(StreamArgs a, cudaStream_t stream) {
   // the time to join a split slab.
   double best = 1e30;
   int best_clusters = 0;
-  for (int C = 1; C <= kMaxCluster && C <= a.p.kt; ++C) {
-    // (the parts of 64 rows by three CTAs would not fit in shared memory)
-    const int clusters = C * ((NT / 16 + C - 1) / C) <= 4 ? max_clusters<NT>(C) : 0;
+  for (int C = 1; C <= kMaxStreamCluster && C <= a.p.kt; ++C) {
+    // (of 64 rows, the parts of three CTAs would not fit in shared memory)
+    const int clusters = C * ((NT / 16 + C - 1) / C) <= StreamCfg<NT>::kChunks ? max_clusters<NT>(C) : 0;
     if (clusters < 1) continue;
     const int tiles = (a.p.kt + C - 1) / C;
     auto round_us = [&](int n) {
@@ -496,7 +500,7 @@ w8a8_status run(StreamArgs a, cudaStream_t stream) {
   if (!best_clusters) return W8A8_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(best_clusters * a.C));
-  cfg.blockDim = dim3(kStreamThreads + (QUANT ? 32 * kQuantWarps : 0));
+  cfg.blockDim = dim3(StreamCfg<NT>::kThreads + (QUANT ? 32 * kQuantWarps : 0));
   cfg.dynamicSmemBytes = (size_t)StreamCfg<NT>::kAlloc;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -525,7 +529,8 @@ w8a8_status launch_mx4_stream(const Mx4Args &p, const void *x, int64_t ldx, int6
   if (x) return run<16, true>(a, stream);
   if (p.M <= 16) return run<16, false>(a, stream);
   if (p.M <= 32) return run<32, false>(a, stream);
-  return run<64, false>(a, stream);
+  if (p.M <= 64) return run<64, false>(a, stream);
+  return run<128, false>(a, stream);
 }
 
 }  // namespace w8a8
