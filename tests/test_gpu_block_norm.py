@@ -230,3 +230,18 @@ def test_no_groups_refused():
         for i in (None, index):
             with pytest.raises(ValueError, match="groups"):
                 w8.block_norm(x, r, group_index=i, **kw)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,K", [(3700, 4096), (3700, 3600), (2500, 5120), (1300, 6160), (700, 8208), (20, 4112)])
+def test_y_alone_and_codes_alone_agree(M, K, dtype):
+    """However many rows: the codes of one call are those of another call's y."""
+    x, r, (pw, pb), (w, b), (gate, scale, shift) = tensors(M + K, M, K, 2, dtype)
+    kw = dict(post=w8.Norm("rms", pw, pb), gate=gate, pre=w8.Norm("layer", w, b), scale=scale, shift=shift,
+              rows_per_group=M // 2 + 1)
+    y = w8.block_norm(x, r, **kw)
+    four, eight = w8.block_norm(x, r, codes="mx4", **kw), w8.block_norm(x, r, codes="int8", **kw)
+    assert torch.equal(four.residual, y.residual) and torch.equal(eight.residual, y.residual)
+    assert all(torch.equal(p, q) for p, q in zip(four.mx4.unpack(), w8.mx4_quant(y.y).unpack()))
+    q, s = w8.quant_act(y.y)
+    assert torch.equal(eight.q, q) and torch.equal(eight.a_scale, s)

@@ -601,14 +601,15 @@ extern "C" w8a8_status w8a8_block_norm(const w8a8_block_norm_args *p, w8a8_strea
   // may not fit twice).  Three if that makes a quarter more warps than two:
   // both norms, 4096 x 5120 60 us with two (10 warps), 45 with three (14);
   // but 4096 x 7168 67 with two (14), 76 with three (10).  Four with 160
-  // registers for many rows a CTA, without an fp32 residual or an image, if at
-  // most a quarter of the warps is lost: a row takes longer, but fewer
-  // instructions (8192 x 4096 59 us, with two chunks 67; 1000 x 4096 13.9 and
-  // 13.0; 4096 x 4096 with an fp32 residual 44.1 and 43.1; to 4-bit codes 31.4
-  // and 30.4; 4096 x 8192, half the warps, 77 and 68).  Past 8192 three, where
-  // they suffice (4000 x 10240, fp32 residual, 116 us; with four 175).  An
-  // image's padding columns count (the lanes that hold them write them).
-  const int64_t nchunks = a.image ? (int64_t)a.kt * 32 : K / 8;
+  // registers for many rows a CTA without an fp32 residual, if at most a
+  // quarter of the warps is lost: a row takes longer, but fewer instructions
+  // (8192 x 4096 59 us, with two chunks 67; 1000 x 4096 13.9 and 13.0; 4096 x
+  // 4096 with an fp32 residual 44.1 and 43.1; 4096 x 8192, half the warps, 77
+  // and 68).  Past 8192 three, where they suffice (4000 x 10240, fp32 residual,
+  // 116 us; with four 175).  The outputs have no say: y has the same bits
+  // beside codes or alone.  An image's padding columns only add warps (the
+  // lanes that hold them write them).
+  int64_t nchunks = K / 8;
   int cpl = 2, regs = 128;
   int64_t resident = 0, smem = 0;
   auto shape = [&](int c, int r) {
@@ -632,9 +633,13 @@ extern "C" w8a8_status w8a8_block_norm(const w8a8_block_norm_args *p, w8a8_strea
   } else {
     const int64_t three = warps(3, 128), two = warps(2, 128);
     const int c = three * 4 > two * 5 ? 3 : 2;
-    const bool four = !a.residual_f32 && !a.image && warps(4, 160) * 4 >= (c == 3 ? three : two) * 3 &&
+    const bool four = !a.residual_f32 && warps(4, 160) * 4 >= (c == 3 ? three : two) * 3 &&
                       M >= 8 * resident;
     if (!four) shape(c, 128);
+  }
+  if (a.image) {
+    nchunks = (int64_t)a.kt * 32;
+    shape(cpl, regs);
   }
   if (smem > kMaxFolded) return W8A8_ERR_UNSUPPORTED_SHAPE;
   cudaLaunchConfig_t cfg = {};
