@@ -152,3 +152,17 @@ def test_reference_pins():
         x = np.zeros((1, 32))
         x[0, 0], x[0, 1], x[0, 2] = 4.0, lo + 0.49 * (hi - lo), lo + 0.51 * (hi - lo)
         assert ref.values(*ref.encode(x))[0, 1:3].tolist() == [lo, hi]
+
+
+def test_vectors_of_several_groups_need_a_grouping():
+    import w8a8_int8_dynamic_b200 as w8
+    x, v = torch.zeros(6, 64, dtype=torch.bfloat16), torch.zeros(2, 64, dtype=torch.bfloat16)
+    n = w8.Norm("rms")
+    for kw in (dict(gate=v), dict(pre=n, scale=v), dict(pre=n, shift=v), dict(gate=v[:1], pre=n, scale=v)):
+        with pytest.raises(ValueError, match="rows_per_group or group_index"):
+            w8.block_norm(x, x, **kw)
+    # what has a grouping, or needs none, goes on to the next check
+    for kw in (dict(gate=v, rows_per_group=3), dict(gate=v, group_index=torch.zeros(6, dtype=torch.int32)), dict(gate=v[:1]),
+               dict(gate=v[0])):
+        with pytest.raises(ValueError, match="CUDA tensor"):
+            w8.block_norm(x, x, **kw)

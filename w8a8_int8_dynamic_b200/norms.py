@@ -85,11 +85,16 @@ def block_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, *, post
     for an update in place) or to a new tensor.
     gate, scale, shift: bf16 [groups, K] (slices of a wider tensor may be given as they are; [K]
     for one group).  The group of row m is ``group_index[m]`` (int32; a row whose index is
-    outside the groups, or negative where none of the three is given, is padding and is left alone), else m // ``rows_per_group`` (default: all
-    rows in one group).
+    outside the groups, or negative where none of the three is given, is padding and is left alone),
+    else m // ``rows_per_group``; one of the two has to be given where there are several groups
+    (a single one takes all rows).
     codes: "int8" (``q`` and ``a_scale``, for ``W8A8Linear.apply_codes``) or "mx4" (an ``MX4Tensor``, for
     ``MX4Linear``), equal to the codes of the bf16 output; None: y itself.  ``y=True`` gives y beside codes.
     """
+    if rows_per_group is None and group_index is None:
+        for t, name in ((gate, "gate"), (scale, "scale"), (shift, "shift")):
+            if t is not None and t.dim() > 1 and t.shape[0] > 1:
+                raise ValueError(f"{name} holds {t.shape[0]} groups: give rows_per_group or group_index")
     _need_cuda(x, "x", torch.bfloat16)
     K = x.shape[-1]
     if codes not in (None, "int8", "mx4"):
