@@ -388,7 +388,7 @@ typedef enum { W8A8_NORM_NONE = 0, W8A8_NORM_RMS = 1, W8A8_NORM_LAYER = 2 } w8a8
 typedef enum { W8A8_DTYPE_BF16 = 0, W8A8_DTYPE_FP32 = 1 } w8a8_dtype;
 
 typedef struct {
-  int kind;           /* w8a8_norm_kind */
+  int kind;           /* w8a8_norm_kind; with W8A8_NORM_NONE the rest is not looked at */
   float eps;          /* > 0 */
   const void *weight; /* device, bf16 [K], or NULL */
   const void *bias;   /* device, bf16 [K], or NULL */

@@ -5,6 +5,8 @@ import torch
 
 import w8a8_int8_dynamic_b200 as w8
 from gpu_util import require_gpu
+from w8a8_int8_dynamic_b200.binding import _raw_stream, lib
+from w8a8_int8_dynamic_b200.norms import _ARGS
 
 pytestmark = pytest.mark.gpu
 
@@ -245,3 +247,17 @@ def test_y_alone_and_codes_alone_agree(M, K, dtype):
     assert all(torch.equal(p, q) for p, q in zip(four.mx4.unpack(), w8.mx4_quant(y.y).unpack()))
     q, s = w8.quant_act(y.y)
     assert torch.equal(eight.q, q) and torch.equal(eight.a_scale, s)
+
+
+def test_vectors_of_no_norm_are_not_looked_at():
+    """The C call with kind NONE and a weight, bias and eps beside it: u is x, whatever they hold."""
+    M, K = 5, 272
+    x, r, (w, b), _, (gate, _, _) = tensors(23, M, K, 1)
+    want = w8.block_norm(x, r, gate=gate)
+    out = torch.empty_like(r)
+    for weight, bias in ((w.data_ptr(), 0), (0, b.data_ptr()), (w.data_ptr(), b.data_ptr()), (2, 2)):
+        norm = (0, float("nan"), weight, bias)
+        args = _ARGS.pack(M, K, x.data_ptr(), K, r.data_ptr(), out.data_ptr(), K, K, 0, 1.0, *norm, *norm,
+                          gate.data_ptr(), 0, 0, K, 0, 0, 1, M, 0, 0, 0, 0, 0, 0, 0)
+        assert lib().w8a8_block_norm(args, _raw_stream(0)) == 0
+        assert torch.equal(out, want.residual)

@@ -557,9 +557,11 @@ extern "C" w8a8_status w8a8_block_norm(const w8a8_block_norm_args *p, w8a8_strea
   if (mod && p->groups > 0x7FFFFFFF) return W8A8_ERR_INVALID_ARG;
   if (K % ((p->q || p->image) ? 16 : 8) != 0 || K > kMaxNormK) return W8A8_ERR_UNSUPPORTED_SHAPE;
   const void *ptrs[] = {p->x, p->residual, p->residual_out, p->y, p->q, p->a_scale, p->image, p->gate,
-                        p->scale, p->shift, p->post.weight, p->post.bias, p->pre.weight, p->pre.bias};
+                        p->scale, p->shift};
   for (const void *q : ptrs)
     if (!aligned16(q)) return W8A8_ERR_ALIGNMENT;
+  for (const w8a8_norm *n : {&p->post, &p->pre})
+    if (n->kind != W8A8_NORM_NONE && (!aligned16(n->weight) || !aligned16(n->bias))) return W8A8_ERR_ALIGNMENT;
   if (reinterpret_cast<uintptr_t>(p->group_index) & 3u) return W8A8_ERR_ALIGNMENT;
   const int64_t re = p->residual_dtype == W8A8_DTYPE_FP32 ? 4 : 8;
   if (p->ldx % 8 || (res && (p->ldr % re || p->ldro % re)) || (p->y && p->ldy % 8) ||
@@ -575,10 +577,14 @@ extern "C" w8a8_status w8a8_block_norm(const w8a8_block_norm_args *p, w8a8_strea
   a.q = p->q;
   a.a_scale = p->a_scale;
   a.image = static_cast<uint8_t *>(p->image);
-  a.post_w = static_cast<const uint16_t *>(p->post.weight);
-  a.post_b = static_cast<const uint16_t *>(p->post.bias);
-  a.pre_w = static_cast<const uint16_t *>(p->pre.weight);
-  a.pre_b = static_cast<const uint16_t *>(p->pre.bias);
+  if (p->post.kind != W8A8_NORM_NONE) {  // (without the norm its vectors are not looked at)
+    a.post_w = static_cast<const uint16_t *>(p->post.weight);
+    a.post_b = static_cast<const uint16_t *>(p->post.bias);
+  }
+  if (p->pre.kind != W8A8_NORM_NONE) {
+    a.pre_w = static_cast<const uint16_t *>(p->pre.weight);
+    a.pre_b = static_cast<const uint16_t *>(p->pre.bias);
+  }
   a.gate = static_cast<const uint16_t *>(p->gate);
   a.scale = static_cast<const uint16_t *>(p->scale);
   a.shift = static_cast<const uint16_t *>(p->shift);
