@@ -261,3 +261,13 @@ def test_vectors_of_no_norm_are_not_looked_at():
                           gate.data_ptr(), 0, 0, K, 0, 0, 1, M, 0, 0, 0, 0, 0, 0, 0)
         assert lib().w8a8_block_norm(args, _raw_stream(0)) == 0
         assert torch.equal(out, want.residual)
+
+
+@pytest.mark.parametrize("K", [264, 1000, 5120, 14336])
+def test_layer_norm_of_rows_far_from_zero(K):
+    """A mean whose square is no float: the squares that the norm takes are of the differences."""
+    g = torch.Generator(device="cuda").manual_seed(K)
+    x = ((1 + torch.randint(0, 2, (5, K), device="cuda", generator=g) / 128) * 2.0 ** 65).bfloat16()
+    x[1] *= -1
+    kw = dict(pre=w8.Norm("layer", eps=1e-6))
+    check(w8.block_norm(x, **kw), x, None, kw, np.zeros(5, int))

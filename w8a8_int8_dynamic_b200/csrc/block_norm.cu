@@ -158,8 +158,9 @@ __device__ __forceinline__ Stat centre(Eight (&t)[CPL], int kind, float eps, flo
   if (at.W > 1) {
     if (at.lane == 0) line[at.w] = make_float2(own, m2);
     __syncthreads();
-    float2 part = make_float2(0.0f, 0.0f);
-    if (at.lane < at.W) part = line[at.lane];
+    // (a lane without a part stands at the first one's mean: its distance, times a count of zero, is no NaN)
+    float2 part = line[at.lane < at.W ? at.lane : 0];
+    if (at.lane >= at.W) part.y = 0.0f;
     if (layer) {
       const float mean = half_sum(part.x * at.lane_count) * inv_k;
       const float d = part.x - mean;
