@@ -271,3 +271,18 @@ def test_layer_norm_of_rows_far_from_zero(K):
     x[1] *= -1
     kw = dict(pre=w8.Norm("layer", eps=1e-6))
     check(w8.block_norm(x, **kw), x, None, kw, np.zeros(5, int))
+
+
+@pytest.mark.parametrize("K", [8, 24, 1000, 4104, 5120, 8200, 12304, 14336])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_layer_norm_of_constant_rows_is_the_bias(K, dtype):
+    """The sum of a row of equal bf16 values is exact in fp32 (8 bits and 14 of the count), so is its mean: nothing is
+    left for 1 / sqrt(eps) to enlarge, before the block or after it."""
+    values = torch.tensor([1000.0, -3.140625, 0.01, 57344.0, 1 / 3, 1e4, 0.0, -2.0 ** 100], device="cuda").bfloat16()
+    rows = values.view(-1, 1).repeat(1, K)
+    _, r, (w, b), _, _ = tensors(K, len(values), K)
+    n = w8.Norm("layer", w, b, 1e-6)
+    for out in (w8.block_norm(rows, pre=n), w8.block_norm(torch.zeros_like(rows), rows.to(dtype), pre=n)):
+        assert torch.equal(out.y, b.expand_as(rows))
+    r = r.to(dtype)
+    assert torch.equal(w8.block_norm(rows, r, post=w8.Norm("layer", w, eps=1e-6)).residual, r)
