@@ -296,3 +296,26 @@ def test_pack_of_other_than_a_matrix_refused():
     for c, s in ((codes, scales), (codes, scales[:, 0]), (codes[0, 0], scales[0, 0])):
         with pytest.raises(ValueError):
             w8.mx4_pack(c, s)
+
+
+@pytest.mark.parametrize("width", [400, 404])
+@pytest.mark.parametrize("M", [1, 5, 40])
+def test_slices_at_any_element(M, width):
+    """A start that is no 16-byte boundary, in a parent whose rows are on them and in one whose are not."""
+    wide = sample(np.random.default_rng(M), M, width)
+    x, w, b = wide[:, 4:276], *operands(1, 1, 272, 272)[1:]
+    c = x.contiguous()
+    offset = torch.empty(M * 272 + 4, dtype=torch.bfloat16, device="cuda")[4:].view(M, 272).copy_(c)
+    n, mod = w8.Norm("layer"), wide[:1, 100:372].contiguous()
+    want, stream = w8.block_norm(c, c.float(), gate=mod, pre=n, shift=mod, codes="int8"), w8.block_norm(c, c, gate=mod).residual
+    codes, scales = w.unpack()
+    for v in (x, offset):
+        assert all(torch.equal(p, q) for p, q in zip(w8.mx4_quant(v).unpack(), w8.mx4_quant(c).unpack()))
+        assert torch.equal(w8.mx4_linear(v, w, b), w8.mx4_linear(c, w, b))
+        assert all(torch.equal(p, q) for p, q in zip(w8.mx4_linear_quant(v, w).unpack(), w8.mx4_linear_quant(c, w).unpack()))
+        got = w8.block_norm(v, v.float(), gate=wide[0, 100:372], pre=n, shift=wide[:1, 100:372], codes="int8")
+        assert torch.equal(got.residual, want.residual) and torch.equal(got.q, want.q) and torch.equal(got.a_scale, want.a_scale)
+        assert torch.equal(w8.block_norm(v, v, gate=wide[:1, 100:372]).residual, stream)
+    # a weight's rows cut out of a taller one
+    lone = torch.empty(codes.numel() + 8, dtype=torch.uint8, device="cuda")[8:].view(codes.shape).copy_(codes)
+    assert all(torch.equal(p, q) for p, q in zip(w8.mx4_pack(lone, scales).unpack(), (codes, scales)))

@@ -166,3 +166,23 @@ def test_vectors_of_several_groups_need_a_grouping():
                dict(gate=v[0])):
         with pytest.raises(ValueError, match="CUDA tensor"):
             w8.block_norm(x, x, **kw)
+
+
+def test_rows_are_on_16_byte_boundaries_whatever_the_slice():
+    """What the calls hand to the library: the tensor itself where that is possible, else a copy."""
+    from w8a8_int8_dynamic_b200.binding import _rows_of
+    base = torch.randn(13 * 48 * 8).bfloat16()
+    assert base.data_ptr() % 16 == 0
+    for width in (40, 44, 48):
+        wide = base[:6 * 2 * width].view(6, 2, width)
+        for x, same in ((wide[..., :40], None), (wide[:, 0, :40], None), (wide[:, 0, 4:36], False), (wide[:, 1, 8:40], None),
+                        (wide[2:3, 1, 4:36], None), (base[4:132].view(4, 32), False), (base[8:136].view(4, 32), True),
+                        (wide[..., 0:32:2], False), (wide[:, :, 4:36], False), (base[:32].expand(3, 32), False)):
+            x2, rows, ld = _rows_of(x)
+            assert x2.data_ptr() % 16 == 0 and (rows == 1 or ld % 8 == 0) and x2.stride(-1) == 1
+            K = x.shape[-1]
+            assert rows == x.numel() // K and ld >= K
+            got = torch.as_strided(x2, (rows, K), (ld, 1), x2.storage_offset())
+            assert torch.equal(got, x.reshape(rows, K))
+            if same is not None:
+                assert (x2.data_ptr() == x.data_ptr()) == same

@@ -190,13 +190,14 @@ def _size(name: str, device: int, *shape: int) -> int:
 
 
 def _rows_of(x: torch.Tensor) -> Tuple[torch.Tensor, int, int]:
-    """[..., K] -> ([rows, K] with unit stride along K and rows on 16-byte boundaries, rows, row stride)."""
+    """[..., K] -> ([rows, K] with unit stride along K and rows on 16-byte boundaries, rows, row stride):
+    x itself, a view or, where its start or its rows are on other boundaries, a copy."""
     K = x.shape[-1]
     if x.is_contiguous():
-        return x, x.numel() // K if K else 0, K
+        return x.clone() if x.data_ptr() & 15 else x, x.numel() // K if K else 0, K
     x2 = x if x.dim() == 2 else x.reshape(-1, K)
     rows, (ld, step) = x2.shape[0], x2.stride()
-    if step != 1 or (rows > 1 and (ld % 8 or ld < K)):
+    if step != 1 or x2.data_ptr() & 15 or (rows > 1 and (ld % 8 or ld < K)):
         x2 = x2.clone(memory_format=torch.contiguous_format)
         ld = K
     return x2, rows, ld if rows > 1 else K

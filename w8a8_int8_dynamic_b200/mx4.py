@@ -123,6 +123,8 @@ def mx4_pack(codes: torch.Tensor, scales: torch.Tensor, image: Optional[torch.Te
             return mx4_pack(codes, scales, image)
     s = _raw_stream(index)
     c, e = codes.contiguous(), scales.contiguous()
+    if c.data_ptr() & 15:
+        c = c.clone()
     out = _image(image, rows, K, index)
     if rows:
         _check(lib().w8a8_mx4_pack(c.data_ptr(), e.data_ptr(), rows, K, out.data_ptr(), out.numel(), s),

@@ -54,7 +54,7 @@ def _vector(t: Optional[torch.Tensor], name: str, K: int) -> int:
 
 
 def _per_group(t: torch.Tensor, name: str, K: int, groups: int):
-    """(t as [groups, K] with rows on 16-byte boundaries, its address, groups, row stride)."""
+    """(t, or a copy of it, as [groups, K] with rows on 16-byte boundaries, its address, groups, row stride)."""
     _need_cuda(t, name, torch.bfloat16)
     if t.dim() == 1:
         t = t.view(1, -1)
@@ -63,8 +63,8 @@ def _per_group(t: torch.Tensor, name: str, K: int, groups: int):
         raise ValueError(f"{name} must be [groups, {K}], with as many groups as the others, got {list(shape)}")
     groups = shape[0]
     ld, step = t.stride()
-    if step != 1 or (groups > 1 and (ld % 8 or ld < K)):
-        t = t.contiguous()
+    if step != 1 or t.data_ptr() & 15 or (groups > 1 and (ld % 8 or ld < K)):
+        t = t.clone(memory_format=torch.contiguous_format)
         ld = K
     return t, t.data_ptr(), groups, ld if groups > 1 else K
 
