@@ -286,3 +286,26 @@ def test_layer_norm_of_constant_rows_is_the_bias(K, dtype):
         assert torch.equal(out.y, b.expand_as(rows))
     r = r.to(dtype)
     assert torch.equal(w8.block_norm(rows, r, post=w8.Norm("layer", w, eps=1e-6)).residual, r)
+
+
+@pytest.mark.parametrize("codes", [None, "int8", "mx4"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_outputs_of_strided_inputs(codes, dtype):
+    """Rows of a wider tensor, a transposed one and a row repeated: every output is dense and that of contiguous copies."""
+    M, K = 24, 528
+    x, r, _, (w, _), (gate, _, _) = tensors(29, M, K, 1, dtype)
+    n = w8.Norm("layer", w)
+    wide_x = torch.zeros(M, 1000, dtype=torch.bfloat16, device="cuda")
+    wide_r = torch.zeros(M, 800, dtype=dtype, device="cuda")
+    wide_x[:, 8:536], wide_r[:, 16:544] = x, r
+    for xs, rs in ((wide_x[:, 8:536], wide_r[:, 16:544]), (x, wide_r[:, 16:544]), (wide_x[:, 8:536], r),
+                   (x.t().contiguous().t(), r.t().contiguous().t()), (x[:1].expand(M, K), r[:1].expand(M, K)),
+                   (wide_x.view(4, 6, 1000)[..., 8:536], wide_r.view(4, 6, 800)[..., 16:544])):
+        kw = dict(gate=gate, pre=n, codes=codes, y=True)
+        got, want = w8.block_norm(xs, rs, **kw), w8.block_norm(xs.contiguous(), rs.contiguous(), **kw)
+        for name in ("residual", "y", "q", "a_scale"):
+            g, v = getattr(got, name), getattr(want, name)
+            assert (g is None) == (v is None) and (v is None or g.is_contiguous() and torch.equal(g, v)), name
+        if codes == "mx4":
+            assert all(torch.equal(g, v) for g, v in zip(got.mx4.unpack(), want.mx4.unpack()))
+        assert torch.equal(w8.block_norm(xs, pre=n).y, w8.block_norm(xs.contiguous(), pre=n).y)

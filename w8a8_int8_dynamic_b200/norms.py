@@ -124,14 +124,14 @@ def block_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, *, post
                               scale=scale, shift=shift, rows_per_group=rows_per_group,
                               group_index=group_index, codes=codes, y=y, residual_out=residual_out)
     x2, M, ldx = _rows_of(x)
-    plain = x2 is x  # contiguous
+    plain = x.is_contiguous()  # outputs of its strides are the dense ones that the kernel writes
     r2 = new = None
     ldr = ldro = dtype = 0
     if residual is not None:
         r2, _, ldr = _rows_of(residual)
         dtype, ldro = _RESIDUAL[residual.dtype], K
         if residual_out is None:
-            new = torch.empty_like(r2) if r2 is residual else _new(x.shape[:-1], K, r2.dtype, index)
+            new = torch.empty_like(residual) if residual.is_contiguous() else _new(x.shape[:-1], K, r2.dtype, index)
         else:  # written in place: a view, never a copy
             new = residual_out
             n2 = new.view(-1, K) if new.is_contiguous() else new
