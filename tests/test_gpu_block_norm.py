@@ -309,3 +309,22 @@ def test_outputs_of_strided_inputs(codes, dtype):
         if codes == "mx4":
             assert all(torch.equal(g, v) for g, v in zip(got.mx4.unpack(), want.mx4.unpack()))
         assert torch.equal(w8.block_norm(xs, pre=n).y, w8.block_norm(xs.contiguous(), pre=n).y)
+
+
+@pytest.mark.parametrize("M,K", [(3, 16384), (2, 15008), (300, 16384), (170, 14352), (160, 12304)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_the_longest_rows(M, K, dtype):
+    """To K = 16384 with three of a group's vectors, one row a CTA and several, and the codes of such rows."""
+    x, r, (pw, pb), (w, b), (gate, scale, shift) = tensors(M + K, M, K, 2, dtype)
+    per = -(-M // 2)
+    for kw in (dict(post=w8.Norm("rms", pw), gate=gate, pre=w8.Norm("layer", w, b), scale=scale, shift=shift, rows_per_group=per),
+               dict(post=w8.Norm("layer", pw, pb), gate=gate, pre=w8.Norm("rms", w), rows_per_group=per)):
+        out = w8.block_norm(x, r, **kw)
+        check(out, x, r, kw, np.arange(M) // per)
+        eight, four = w8.block_norm(x, r, codes="int8", **kw), w8.block_norm(x, r, codes="mx4", **kw)
+        q, s = w8.quant_act(out.y)
+        assert torch.equal(eight.q, q) and torch.equal(eight.a_scale, s)
+        assert all(torch.equal(g, v) for g, v in zip(four.mx4.unpack(), w8.mx4_quant(out.y).unpack()))
+    if K > 14336:  # a fourth vector does not fit beside them
+        with pytest.raises(w8.W8A8Error, match="UNSUPPORTED_SHAPE"):
+            w8.block_norm(x, r, post=w8.Norm("rms", pw, pb), pre=w8.Norm("rms", w, b))
