@@ -201,78 +201,67 @@ __device__ __forceinline__ void store_fold(ulonglong2 *v, int c, const Eight &e)
 }
 
 // Folds the vectors of group g (all threads of the CTA; the caller syncs).
-// Every load of a thread's chunks before the first use: one after another they
-// took 20 us of an 8192 x 4096 launch.
+// The loads of a chunk's vectors are in flight together.
 __device__ __forceinline__ void fold(const NormArgs &a, ulonglong2 *v, int64_t g) {
   const int nchunks = a.K >> 3;
   const uint64_t one = f2_splat(1.0f);
-  constexpr int kAtOnce = 1;
-  auto get = [](const uint16_t *p, int c, uint4 &d) {
-    if (p) d = __ldg(reinterpret_cast<const uint4 *>(p) + c);
-  };
   const uint16_t *gp = a.gate ? a.gate + g * a.ld_gate : nullptr;
   const uint16_t *sp = a.scale ? a.scale + g * a.ld_scale : nullptr;
   const uint16_t *tp = a.shift ? a.shift + g * a.ld_shift : nullptr;
-  for (int c0 = threadIdx.x; c0 < nchunks; c0 += kAtOnce * blockDim.x) {
-    uint4 gate[kAtOnce], pw[kAtOnce], pb[kAtOnce], sc[kAtOnce], w[kAtOnce], b[kAtOnce], sh[kAtOnce];
+  for (int c = threadIdx.x; c < nchunks; c += blockDim.x) {
+    auto get = [&](const uint16_t *p, uint4 &d) {
+      if (p) d = __ldg(reinterpret_cast<const uint4 *>(p) + c);
+    };
+    uint4 gate, pw, pb, sc, w, b, sh;
+    get(gp, gate);
+    get(a.post_w, pw);
+    get(a.post_b, pb);
+    get(sp, sc);
+    get(a.pre_w, w);
+    get(a.pre_b, b);
+    get(tp, sh);
+    ulonglong2 *to = v;
+    auto emit = [&](const Eight &e) {
+      store_fold(to, c, e);
+      to += a.padded * 2;
+    };
+    Eight e{{one, one, one, one}};
+    if (gp) e = widen8(gate);
+    Eight f = e;
+    if (a.post_w) {
+      const Eight m = widen8(pw);
 #pragma unroll
-    for (int k = 0; k < kAtOnce; ++k) {
-      const int c = min(c0 + k * (int)blockDim.x, nchunks - 1);
-      get(gp, c, gate[k]);
-      get(a.post_w, c, pw[k]);
-      get(a.post_b, c, pb[k]);
-      get(sp, c, sc[k]);
-      get(a.pre_w, c, w[k]);
-      get(a.pre_b, c, b[k]);
-      get(tp, c, sh[k]);
+      for (int i = 0; i < 4; ++i) f.p[i] = f2_mul(f.p[i], m.p[i]);
     }
+    if (a.folded & kFoldBranch) emit(f);
+    if (a.folded & kFoldBranchAdd) {
+      f = widen8(pb);
 #pragma unroll
-    for (int k = 0; k < kAtOnce; ++k) {
-      const int c = c0 + k * (int)blockDim.x;
-      if (c >= nchunks) break;
-      ulonglong2 *to = v;
-      auto emit = [&](const Eight &e) {
-        store_fold(to, c, e);
-        to += a.padded * 2;
-      };
-      Eight e{{one, one, one, one}};
-      if (gp) e = widen8(gate[k]);
-      Eight f = e;
-      if (a.post_w) {
-        const Eight m = widen8(pw[k]);
+      for (int i = 0; i < 4; ++i) f.p[i] = f2_mul(f.p[i], e.p[i]);
+      emit(f);
+    }
+    e = {{one, one, one, one}};
+    if (sp) {
+      e = widen8(sc);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f.p[i] = f2_mul(f.p[i], m.p[i]);
+      for (int i = 0; i < 4; ++i) e.p[i] = f2_add(e.p[i], one);
+    }
+    f = e;
+    if (a.pre_w) {
+      const Eight m = widen8(w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f.p[i] = f2_mul(f.p[i], m.p[i]);
+    }
+    if (a.folded & kFoldMul) emit(f);
+    if (a.folded & kFoldAdd) {
+      f = {{0, 0, 0, 0}};
+      if (tp) f = widen8(sh);
+      if (a.pre_b) {
+        const Eight m = widen8(b);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f.p[i] = f2_fma(m.p[i], e.p[i], f.p[i]);
       }
-      if (a.folded & kFoldBranch) emit(f);
-      if (a.folded & kFoldBranchAdd) {
-        f = widen8(pb[k]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f.p[i] = f2_mul(f.p[i], e.p[i]);
-        emit(f);
-      }
-      e = {{one, one, one, one}};
-      if (sp) {
-        e = widen8(sc[k]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) e.p[i] = f2_add(e.p[i], one);
-      }
-      f = e;
-      if (a.pre_w) {
-        const Eight m = widen8(w[k]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f.p[i] = f2_mul(f.p[i], m.p[i]);
-      }
-      if (a.folded & kFoldMul) emit(f);
-      if (a.folded & kFoldAdd) {
-        f = {{0, 0, 0, 0}};
-        if (tp) f = widen8(sh[k]);
-        if (a.pre_b) {
-          const Eight m = widen8(b[k]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) f.p[i] = f2_fma(m.p[i], e.p[i], f.p[i]);
-        }
-        emit(f);
-      }
+      emit(f);
     }
   }
 }
@@ -521,7 +510,9 @@ cudaError_t run(const cudaLaunchConfig_t &cfg, const NormArgs &a) {
 template <int CPL, int REGS>
 cudaError_t run(const cudaLaunchConfig_t &cfg, const NormArgs &a) {
   if (!a.residual) return run<CPL, kNoResidual, REGS>(cfg, a);
-  return a.residual_f32 ? run<CPL, kResidualF32, REGS>(cfg, a) : run<CPL, kResidualBf16, REGS>(cfg, a);
+  if constexpr (REGS <= 128)  // (more are never chosen with an fp32 residual)
+    if (a.residual_f32) return run<CPL, kResidualF32, REGS>(cfg, a);
+  return run<CPL, kResidualBf16, REGS>(cfg, a);
 }
 
 constexpr int64_t kMaxNormK = 16384;
@@ -623,9 +614,9 @@ extern "C" w8a8_status w8a8_block_norm(const w8a8_block_norm_args *p, w8a8_strea
   // 4096 with an fp32 residual 44.1 and 43.1; 4096 x 8192, half the warps, 77
   // and 68).  Past 8192 three, where they suffice (4000 x 10240, fp32 residual,
   // 116 us; with four 175).  The outputs have no say: y has the same bits
-  // beside codes or alone.  An image's padding columns only add warps (the
-  // lanes that hold them write them).
-  int64_t nchunks = K / 8;
+  // beside codes or alone.  (An image's padding columns, to 256, are always
+  // within the warps' parts, whose lanes there write them.)
+  const int64_t nchunks = K / 8;
   int cpl = 2, regs = 128;
   int64_t resident = 0, smem = 0;
   auto shape = [&](int c, int r) {
@@ -652,10 +643,6 @@ extern "C" w8a8_status w8a8_block_norm(const w8a8_block_norm_args *p, w8a8_strea
     const bool four = !a.residual_f32 && warps(4, 160) * 4 >= (c == 3 ? three : two) * 3 &&
                       M >= 8 * resident;
     if (!four) shape(c, 128);
-  }
-  if (a.image) {
-    nchunks = (int64_t)a.kt * 32;
-    shape(cpl, regs);
   }
   if (smem > kMaxFolded) return W8A8_ERR_UNSUPPORTED_SHAPE;
   cudaLaunchConfig_t cfg = {};
