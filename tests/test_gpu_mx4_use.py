@@ -319,3 +319,33 @@ def test_slices_at_any_element(M, width):
     # a weight's rows cut out of a taller one
     lone = torch.empty(codes.numel() + 8, dtype=torch.uint8, device="cuda")[8:].view(codes.shape).copy_(codes)
     assert all(torch.equal(p, q) for p, q in zip(w8.mx4_pack(lone, scales).unpack(), (codes, scales)))
+
+
+@pytest.mark.parametrize("M", [2, 40, 300])
+def test_vectors_and_biases_that_the_kernel_ahead_writes_in_place(M):
+    """Modulation, bias and rows in buffers that every step writes anew just before they are read, by kernels that start
+    while the one ahead, and the reader of the old values before it, still run."""
+    D, steps = 1040, 40
+    rng = np.random.default_rng(M)
+    cond = [sample(rng, 2, D) for _ in range(steps)]
+    make = w8.MX4Linear.from_float(bf(rng.standard_normal((3 * D, D)) * D ** -0.5))
+    layer = w8.mx4_quant(bf(rng.standard_normal((D, D)) * D ** -0.5))
+    x, n = sample(rng, M, D), w8.Norm("layer")
+    per = M // 2
+
+    def step(c, mod, rows):
+        make(c, out=mod)
+        gate, scale, shift = mod.split(D, 1)
+        a = w8.block_norm(x, x, gate=gate, pre=n, scale=scale, shift=shift, rows_per_group=per, codes="mx4")
+        w8.mx4_dequant(a.mx4, out=rows)
+        y = w8.mx4_linear(rows, layer, mod[1, D:2 * D])  # a bias from the same buffer
+        return y, w8.mx4_quant(rows).dequant()
+
+    mod = torch.empty(2, 3 * D, dtype=torch.bfloat16, device="cuda")
+    rows = torch.empty(M, D, dtype=torch.bfloat16, device="cuda")
+    got = [step(c, mod, rows) for c in cond]
+    torch.cuda.synchronize()
+    for c, pair in zip(cond, got):
+        want = step(c, torch.empty_like(mod), torch.empty_like(rows))
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, v) for g, v in zip(pair, want))

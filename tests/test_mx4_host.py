@@ -186,3 +186,23 @@ def test_rows_are_on_16_byte_boundaries_whatever_the_slice():
             assert torch.equal(got, x.reshape(rows, K))
             if same is not None:
                 assert (x2.data_ptr() == x.data_ptr()) == same
+
+
+def test_kernels_that_start_early_read_through_the_coherent_path():
+    """A kernel with a wait for the one ahead runs while that one still writes what it will read: __ldg, ld.global.nc and
+    const __restrict__ parameters promise memory that nothing writes while the kernel runs."""
+    import os
+    import re
+    from w8a8_int8_dynamic_b200 import build
+    seen = 0
+    for name in ("block_norm.cu", "mx4_common.cuh", "mx4_gemm.cu", "mx4_pair.cu", "mx4_quant.cu", "mx4_stream.cu"):
+        text = re.sub(r"//[^\n]*", "", open(os.path.join(build.CSRC, name)).read())
+        assert not re.search(r"\b__ldg\s*\(|global\.nc|ld_stream_u4", text), name
+        for kernel in re.split(r"(?=__global__)", text)[1:]:
+            head, body = kernel.split("{", 1)
+            if "griddep_wait" in body:
+                seen += 1
+                assert "__restrict__" not in head, (name, head)
+            else:
+                assert "griddep_launch_dependents" not in body, (name, head)
+    assert seen == 6

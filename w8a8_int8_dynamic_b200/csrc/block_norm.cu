@@ -32,7 +32,9 @@
 // 8192 x 4096 with both norms took 98 us for 59.)
 //
 // A programmatic dependent that releases the next kernel at its start and
-// touches memory only after its own wait.
+// touches memory only after its own wait; no load takes the read-only path
+// (the kernel ahead may be writing what this one reads when it starts, and the
+// residual may be updated in place).
 #include <algorithm>
 
 #include "mx4_common.cuh"
@@ -87,17 +89,6 @@ __device__ __forceinline__ float pair_sum(uint64_t p) {
   float lo, hi;
   f2_unpack(p, lo, hi);
   return lo + hi;
-}
-
-// 16 bytes that are read once; not through the read-only path, since the
-// residual may be updated in place.
-__device__ __forceinline__ uint4 ld_once(const void *p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p)
-               : "memory");
-  return v;
 }
 
 constexpr int kMaxWarps = 16;  // of a row: lanes 0..15 join their parts
@@ -210,7 +201,7 @@ __device__ __forceinline__ void fold(const NormArgs &a, ulonglong2 *v, int64_t g
   const uint16_t *tp = a.shift ? a.shift + g * a.ld_shift : nullptr;
   for (int c = threadIdx.x; c < nchunks; c += blockDim.x) {
     auto get = [&](const uint16_t *p, uint4 &d) {
-      if (p) d = __ldg(reinterpret_cast<const uint4 *>(p) + c);
+      if (p) d = reinterpret_cast<const uint4 *>(p)[c];
     };
     uint4 gate, pw, pb, sc, w, b, sh;
     get(gp, gate);
@@ -282,16 +273,16 @@ __device__ __forceinline__ void fetch(const uint8_t *x, const uint8_t *r, const 
   for (int j = 0; j < CPL; ++j) {
     const bool in = at.c0 + 32 * j < at.nchunks;
     d.x[j] = make_uint4(0, 0, 0, 0);
-    if (in) d.x[j] = ld_once(x + j * 512);
+    if (in) d.x[j] = ld_once_u4(x + j * 512);
     if constexpr (RES == kResidualF32) {
       d.r0[j] = d.r1[j] = make_uint4(0, 0, 0, 0);
       if (in) {
-        d.r0[j] = ld_once(r + j * 1024);
-        d.r1[j] = ld_once(r + j * 1024 + 16);
+        d.r0[j] = ld_once_u4(r + j * 1024);
+        d.r1[j] = ld_once_u4(r + j * 1024 + 16);
       }
     } else if constexpr (RES == kResidualBf16) {
       d.r0[j] = make_uint4(0, 0, 0, 0);
-      if (in) d.r0[j] = ld_once(r + j * 512);
+      if (in) d.r0[j] = ld_once_u4(r + j * 512);
     }
   }
 }

@@ -238,7 +238,7 @@ __global__ void __maxnreg__(kGemmRegs)
       const uint32_t b = i & 1, bph = (i >> 1) & 1;
       for (int j = lane * 8; j < kCols; j += 256) {
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (args.bias && n0 + j < args.N) v = __ldg(reinterpret_cast<const uint4 *>(args.bias + n0 + j));
+        if (args.bias && n0 + j < args.N) v = *reinterpret_cast<const uint4 *>(args.bias + n0 + j);
         *reinterpret_cast<uint4 *>(s_bias + j) = v;
       }
       __syncwarp();

@@ -257,7 +257,7 @@ __global__ void __maxnreg__(kGemmRegs)
         const int j = lane * 4;  // 4 bias values a lane: chunk j / 32
         const int n = nb * 256 + column(j >> 5) + (j & 31);
         uint2 v = make_uint2(0, 0);
-        if (args.bias && n < args.N) v = __ldg(reinterpret_cast<const uint2 *>(args.bias + n));
+        if (args.bias && n < args.N) v = *reinterpret_cast<const uint2 *>(args.bias + n);
         *reinterpret_cast<uint2 *>(s_bias + j) = v;
       }
       __syncwarp();

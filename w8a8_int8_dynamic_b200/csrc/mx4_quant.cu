@@ -10,9 +10,13 @@
 // (4096 x 4096: 10.1 us; with one row of eight elements a lane 11.7).
 // HBM-bound: 2 bytes read and 17/32 written an element.
 //
-// All kernels of the 4-bit layers are programmatic dependents that release the
-// next kernel at their start and read and write global memory only after their
-// own wait, so any of them may follow any kernel.
+// Quantisation and dequantisation, as the products, are programmatic
+// dependents: they read and write global memory only after their own wait for
+// the kernel ahead, so they may follow any kernel, and never through the
+// read-only path (no __ldg, no const __restrict__ pointers), since the kernel
+// ahead may still be writing when they start.  These two and the few-row
+// product release the next kernel at their start; the two large products do
+// not.  Repack and unpack have no wait: they have to stay ordinary launches.
 #include <algorithm>
 
 #include "mx4_common.cuh"
@@ -30,8 +34,7 @@ __device__ __forceinline__ uint8_t *tile_of(uint8_t *image, int64_t slab, int kt
 
 // grid: (K tiles, row slabs).
 __global__ void __launch_bounds__(kQuantThreads)
-    mx4_quant_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t rows, int K, int kt,
-                     uint8_t *__restrict__ image) {
+    mx4_quant_kernel(const uint16_t *x, int64_t ldx, int64_t rows, int K, int kt, uint8_t *image) {
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31;
@@ -51,8 +54,8 @@ __global__ void __launch_bounds__(kQuantThreads)
     for (int i = 0; i < kQuantBatch; ++i, src += kStep * ldx) {
       v[i][0] = v[i][1] = make_uint4(0, 0, 0, 0);
       if (r0 + i * kStep < nrows && in_k) {
-        v[i][0] = ld_stream_u4(src);
-        v[i][1] = ld_stream_u4(src + 8);
+        v[i][0] = ld_once_u4(src);
+        v[i][1] = ld_once_u4(src + 8);
       }
     }
 #pragma unroll
@@ -127,8 +130,7 @@ __global__ void __launch_bounds__(256)
 // against 23.5).  Every value is exact in bf16 but for scales
 // near the bottom of the range, where the product may be subnormal: rounded.
 __global__ void __launch_bounds__(kQuantThreads)
-    mx4_dequant_kernel(const uint8_t *__restrict__ image, int64_t rows, int K, int kt,
-                       uint16_t *__restrict__ x) {
+    mx4_dequant_kernel(const uint8_t *image, int64_t rows, int K, int kt, uint16_t *x) {
   griddep_launch_dependents();
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

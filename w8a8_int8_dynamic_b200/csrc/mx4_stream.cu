@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(StreamCfg<NT>::kThreads + (QUANT ? 32 * kQuant
       const uint32_t b = i & 1, bph = (i >> 1) & 1;
       const int n = nb * 128 + n_local;
       const float bv =
-          (args.p.bias && n < N) ? __uint_as_float((uint32_t)__ldg(args.p.bias + n) << 16) : 0.0f;
+          (args.p.bias && n < N) ? __uint_as_float((uint32_t)args.p.bias[n] << 16) : 0.0f;
       if (!wait_all(&tfull[b], bph)) break;
       tc_fence_after();
       const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + b * NT;

@@ -455,4 +455,16 @@ __device__ __forceinline__ uint4 ld_stream_u4(const void *p) {
   return v;
 }
 
+// The same through the coherent path: for what the kernel ahead in the stream
+// may have written after this one started (the read-only path is for memory
+// that nothing writes while the kernel runs).
+__device__ __forceinline__ uint4 ld_once_u4(const void *p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
 }  // namespace w8a8
