@@ -312,7 +312,8 @@ w8a8_status w8a8_linear_noalloc(const void *x, int64_t ldx, const void *packed_w
  * 256-element tiles of 17,408 bytes (codes, then scales).  An image of M rows
  * is written for those rows only; rows past M in its last tile keep what
  * they held.  x and weights have the same image, so w8a8_mx4_quant serves for
- * both.  Shape limits and errors as for the int8 layers (K % 16, K <= 131072,
+ * both.  Outputs do not overlap inputs (a product's and a layer's are checked:
+ * W8A8_ERR_INVALID_ARG), but for a layer's y, which may overlap x.  Shape limits and errors as for the int8 layers (K % 16, K <= 131072,
  * N % 8); where the output is an image, N % 16 and N <= 131072 too. */
 
 /* Byte size of the image of a [rows, K] matrix. */
@@ -352,8 +353,9 @@ w8a8_status w8a8_mx4_scaled_mm_quant(const void *a_image, const void *w_image, c
  * dependent of it; up to 16 rows one kernel does both.  The result is that of
  * w8a8_mx4_quant and w8a8_mx4_scaled_mm, bit for bit.  workspace: the image of
  * x, ws_bytes >= w8a8_mx4_linear_workspace_bytes (NULL where that is 0: M <=
- * 16); its contents on entry do not matter, and calls that share one must not
- * overlap. */
+ * 16); its contents on entry do not matter, calls that share one must not
+ * overlap, and it overlaps neither x nor y.  Where y overlaps x, any M needs
+ * w8a8_mx4_bytes(M, K). */
 w8a8_status w8a8_mx4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t *bytes);
 w8a8_status w8a8_mx4_linear(const void *x, int64_t ldx, const void *w_image, const void *bias, void *y,
                             int64_t M, int64_t N, int64_t K, int act, void *workspace, size_t ws_bytes,

@@ -349,3 +349,43 @@ def test_vectors_and_biases_that_the_kernel_ahead_writes_in_place(M):
         want = step(c, torch.empty_like(mod), torch.empty_like(rows))
         torch.cuda.synchronize()
         assert all(torch.equal(g, v) for g, v in zip(pair, want))
+
+
+@pytest.mark.parametrize("M", [1, 4, 16, 17, 200])
+def test_a_layer_in_place(M):
+    """y over x, whole or shifted, however few the rows: the layer is that of quantisation and product."""
+    K = 2048
+    x, w, b = operands(M, M, K, K)
+    want = w8.mx4_scaled_mm(w8.mx4_quant(x), w, b)
+    for _ in range(20):
+        v = x.clone()
+        assert w8.mx4_linear(v, w, b, out=v).data_ptr() == v.data_ptr() and torch.equal(v, want)
+        both = torch.zeros(2 * M + 40, K, dtype=torch.bfloat16, device="cuda")
+        both[1:M + 1] = x
+        w8.mx4_linear(both[1:M + 1], w, b, out=both[:M])
+        assert torch.equal(both[:M], want) and not both[M + 1:].any()
+        both[:M] = x
+        image = both.view(torch.uint8).view(-1)[:w8.mx4_bytes(M, K)]
+        t = w8.mx4_linear_quant(both[:M], w, b, image=image)
+        assert all(torch.equal(p, q) for p, q in zip(t.unpack(), w8.mx4_quant(want).unpack()))
+    layer = w8.MX4Linear(*w.unpack(), b)
+    v = x.clone()
+    assert torch.equal(layer(v, out=v), want)
+    t = w8.mx4_quant(x)
+    with pytest.raises(w8.W8A8Error, match="INVALID_ARG"):
+        w8.mx4_scaled_mm_quant(t, w, b, image=t.image)
+
+
+@pytest.mark.parametrize("M", [1, 16, 17])
+def test_a_wide_layer_over_its_input(M):
+    """More weight slabs than SMs: x is still read when the first outputs are stored."""
+    N, K = 40960, 5120
+    g = torch.Generator(device="cuda").manual_seed(M)
+    x = torch.randn(M, K, device="cuda", generator=g).bfloat16()
+    w = w8.mx4_quant(torch.randn(N, K, device="cuda", generator=g).mul_(K ** -0.5).bfloat16())
+    b = torch.randn(N, device="cuda", generator=g).bfloat16()
+    want = w8.mx4_scaled_mm(w8.mx4_quant(x), w, b)
+    for _ in range(5):
+        buffer = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")
+        v = buffer.view(-1)[:M * K].view(M, K).copy_(x)
+        assert torch.equal(w8.mx4_linear(v, w, b, out=buffer), want)

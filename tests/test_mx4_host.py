@@ -206,3 +206,25 @@ def test_kernels_that_start_early_read_through_the_coherent_path():
             else:
                 assert "griddep_launch_dependents" not in body, (name, head)
     assert seen == 6
+
+
+def test_products_refuse_outputs_over_their_inputs(L):
+    """Host checks alone: none of these addresses is one of memory, and every call is refused."""
+    A, W, B, Y, WS = (ctypes.c_void_p(n << 24) for n in range(1, 6))
+    M, N, K = 20, 256, 512
+    image = 2 * 17408                                            # of x
+    inputs = [(A, image), (W, 4 * 17408), (B, 512)]
+    y = calls(L.w8a8_mx4_scaled_mm, (A, W, B, Y, M, N, K, 0, None))
+    i = calls(L.w8a8_mx4_scaled_mm_quant, (A, W, B, Y, BIG, M, N, K, 0, None))
+    for at, size in inputs:
+        for end in (at.value, at.value + size - 16):
+            assert y(a3=ctypes.c_void_p(end)) == i(a3=ctypes.c_void_p(end)) == 1
+        assert y(a3=ctypes.c_void_p(at.value - M * N * 2 + 16)) == i(a3=ctypes.c_void_p(at.value - 17408 + 16)) == 1
+    n = calls(L.w8a8_mx4_linear, (A, K, W, B, Y, M, N, K, 0, WS, BIG, None))
+    m = calls(L.w8a8_mx4_linear_quant, (A, K, W, B, Y, BIG, M, N, K, 0, WS, BIG, None))
+    for at in (W, B):
+        assert n(a4=at) == m(a4=at) == n(a4=at, a5=4) == m(a4=at, a6=4) == 1
+    for at in (A, Y):
+        assert n(a9=at) == m(a10=at) == 1
+    # few rows in place need the image of x
+    assert n(a4=A, a5=4, a9=None) == m(a4=A, a6=4, a10=None) == n(a4=A, a5=4, a10=image - 1) == m(a4=A, a6=4, a11=100) == 1

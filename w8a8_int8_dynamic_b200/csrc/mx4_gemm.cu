@@ -401,6 +401,20 @@ w8a8_status check_product(const void *w_image, const void *bias, const void *y, 
   return W8A8_OK;
 }
 
+bool overlap(const void *p, size_t np, const void *q, size_t nq) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return p && q && a < b + nq && b < a + np;
+}
+
+size_t output_bytes(bool image, int64_t M, int64_t N) {
+  return image ? (size_t)mx4_image_bytes(M, N) : (size_t)M * N * 2;
+}
+
+// What a product writes while it still reads its operands.
+bool over_weights(const void *out, size_t bytes, const void *w_image, const void *bias, int64_t N, int64_t K) {
+  return overlap(out, bytes, w_image, (size_t)mx4_image_bytes(N, K)) || overlap(out, bytes, bias, (size_t)N * 2);
+}
+
 w8a8_status product(const void *a_image, const void *w_image, const void *bias, void *y, void *y_image,
                     size_t y_image_bytes, bool image, int64_t M, int64_t N, int64_t K, int act,
                     w8a8_stream_t stream) {
@@ -408,6 +422,11 @@ w8a8_status product(const void *a_image, const void *w_image, const void *bias, 
   if (const w8a8_status s = check_product(w_image, bias, y, y_image, image, M, N, K, act)) return s;
   if (!aligned16(a_image)) return W8A8_ERR_ALIGNMENT;
   if (image && y_image_bytes < (size_t)mx4_image_bytes(M, N)) return W8A8_ERR_BUFFER_TOO_SMALL;
+  const void *out = image ? y_image : y;
+  const size_t out_bytes = output_bytes(image, M, N);
+  if (overlap(out, out_bytes, a_image, (size_t)mx4_image_bytes(M, K)) ||
+      over_weights(out, out_bytes, w_image, bias, N, K))
+    return W8A8_ERR_INVALID_ARG;
   return launch_mx4(a_image, w_image, bias, image ? nullptr : y, image ? y_image : nullptr, M, N, K,
                     act, nullptr, 0, reinterpret_cast<cudaStream_t>(stream));
 }
@@ -427,8 +446,17 @@ w8a8_status layer(const void *x, int64_t ldx, const void *w_image, const void *b
   if ((image && y_image_bytes < (size_t)mx4_image_bytes(M, N)) ||
       (workspace ? ws_bytes : 0) < (size_t)layer_workspace_bytes(M, K))
     return W8A8_ERR_BUFFER_TOO_SMALL;
+  const void *out = image ? y_image : y;
+  const size_t out_bytes = output_bytes(image, M, N), a_bytes = (size_t)mx4_image_bytes(M, K);
+  const size_t x_bytes = (size_t)((M - 1) * ldx + K) * 2;
+  // A layer in place: the kernel that quantises x itself would write y where
+  // other CTAs still read x, so x is quantised first, as with more rows.
+  const bool fused = M <= kStreamQuantRows && !overlap(out, out_bytes, x, x_bytes);
+  if (over_weights(out, out_bytes, w_image, bias, N, K) ||
+      (!fused && ((workspace ? ws_bytes : 0) < a_bytes || overlap(workspace, a_bytes, x, x_bytes) ||
+                  overlap(workspace, a_bytes, out, out_bytes))))
+    return W8A8_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const bool fused = M <= kStreamQuantRows;
   if (!fused)
     if (const w8a8_status r = launch_mx4_quant(x, M, K, ldx, workspace, s)) return r;
   return launch_mx4(workspace, w_image, bias, image ? nullptr : y, image ? y_image : nullptr, M, N, K, act,

@@ -65,6 +65,17 @@ def _output(out: Optional[torch.Tensor], lead: Tuple[int, ...], N: int, index: i
     return out.view(*lead, N)
 
 
+def _image_of_x(x2: torch.Tensor, M: int, K: int, ldx: int, out: Optional[torch.Tensor]) -> int:
+    """Bytes of workspace that a layer needs: up to 16 rows none, but where the output is in x's place."""
+    if M <= 16:
+        if out is None:
+            return 0
+        first, last = x2.data_ptr(), x2.data_ptr() + 2 * ((M - 1) * ldx + K)
+        if out.data_ptr() >= last or first >= out.data_ptr() + out.numel() * out.element_size():
+            return 0
+    return mx4_bytes(M, K)
+
+
 def _scratch(workspace: Optional[torch.Tensor], need: int, index: int) -> Tuple[Optional[torch.Tensor], int]:
     if workspace is None:
         return (_bytes(need, index), need) if need else (None, 0)
@@ -203,7 +214,8 @@ def mx4_scaled_mm_quant(a: MX4Tensor, w: MX4Tensor, bias: Optional[torch.Tensor]
 def mx4_linear(x: torch.Tensor, w: MX4Tensor, bias: Optional[torch.Tensor] = None,
                out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                stream=None, act: int = ACT_NONE) -> torch.Tensor:
-    """The whole layer: y[..., N] = x[..., K] quantised, times w (``act``: epilogue activation)."""
+    """The whole layer: y[..., N] = x[..., K] quantised, times w (``act``: epilogue activation).
+    ``out`` may be x or overlap it."""
     _weight(w, bias, x.shape[-1])
     return _linear(x, w, bias, out, workspace, stream, act)
 
@@ -219,7 +231,7 @@ def _linear(x, w, bias, out, workspace, stream, act):
     N, K = w.rows, w.K
     y = _output(out, x.shape[:-1], N, index)
     if M:
-        ws, nbytes = _scratch(workspace, 0 if M <= 16 else mx4_bytes(M, K), index)
+        ws, nbytes = _scratch(workspace, _image_of_x(x2, M, K, ldx, out), index)
         _check(lib().w8a8_mx4_linear(x2.data_ptr(), ldx, w.image.data_ptr(), _at(bias), y.data_ptr(), M, N, K,
                                      act, _at(ws), nbytes, _raw_stream(index)), "w8a8_mx4_linear")
     return y
@@ -245,7 +257,7 @@ def _linear_quant(x, w, bias, image, workspace, stream, act):
     N, K = w.rows, w.K
     y = _image(image, M, N, index)
     if M:
-        ws, nbytes = _scratch(workspace, 0 if M <= 16 else mx4_bytes(M, K), index)
+        ws, nbytes = _scratch(workspace, _image_of_x(x2, M, K, ldx, image), index)
         _check(lib().w8a8_mx4_linear_quant(x2.data_ptr(), ldx, w.image.data_ptr(), _at(bias), y.data_ptr(),
                                            y.numel(), M, N, K, act, _at(ws), nbytes, _raw_stream(index)),
                "w8a8_mx4_linear_quant")
