@@ -384,8 +384,10 @@ w8a8_status w8a8_mx4_linear_quant(const void *x, int64_t ldx, const void *w_imag
  * post.bias, one of gate and post.weight, one of pre.weight and scale, and one
  * of pre.bias and shift are all given: a group's vectors are kept in shared
  * memory), strides in elements and multiples of 16 bytes, all pointers
- * 16-byte aligned (group_index 4).  residual_out may be residual (with the same stride);
- * otherwise outputs do not overlap inputs. */
+ * 16-byte aligned (group_index 4).  residual_out and y may each be residual or x
+ * (with the same stride and type, so that they are the same elements);
+ * otherwise outputs do not overlap inputs or one another (of these four it is
+ * checked: W8A8_ERR_INVALID_ARG). */
 typedef enum { W8A8_NORM_NONE = 0, W8A8_NORM_RMS = 1, W8A8_NORM_LAYER = 2 } w8a8_norm_kind;
 typedef enum { W8A8_DTYPE_BF16 = 0, W8A8_DTYPE_FP32 = 1 } w8a8_dtype;
 

@@ -328,3 +328,33 @@ def test_the_longest_rows(M, K, dtype):
     if K > 14336:  # a fourth vector does not fit beside them
         with pytest.raises(w8.W8A8Error, match="UNSUPPORTED_SHAPE"):
             w8.block_norm(x, r, post=w8.Norm("rms", pw, pb), pre=w8.Norm("rms", w, b))
+
+
+@pytest.mark.parametrize("M", [1, 5, 2500])
+def test_the_stream_over_its_inputs(M):
+    """residual_out as residual, as x, and as columns or rows beside them; other overlaps are refused."""
+    K, wide = 272, 800
+    x, r, (pw, _), (w, _), (gate, _, _) = tensors(31, M, K, 1)
+    kw = dict(post=w8.Norm("layer", pw), gate=gate, residual_scale=0.7, pre=w8.Norm("rms", w))
+    want = w8.block_norm(x, r, **kw)
+    buffer = torch.zeros(M, wide, dtype=torch.bfloat16, device="cuda")
+    for a, b in ((0, 0), (0, 272), (0, 528), (528, 0), (272, 0)):
+        buffer.zero_()
+        buffer[:, a:a + K] = r
+        out = w8.block_norm(x, buffer[:, a:a + K], residual_out=buffer[:, b:b + K], **kw)
+        assert torch.equal(buffer[:, b:b + K], want.residual) and torch.equal(out.y, want.y)
+        assert a == b or torch.equal(buffer[:, a:a + K], r)
+    over = x.clone()
+    out = w8.block_norm(over, r, residual_out=over, **kw)
+    assert torch.equal(over, want.residual) and torch.equal(out.y, want.y)
+    line = torch.zeros(3 * M, K, dtype=torch.bfloat16, device="cuda")
+    line[M:2 * M] = r
+    for at in (0, 2 * M):  # rows ahead and behind
+        w8.block_norm(x, line[M:2 * M], residual_out=line[at:at + M], **kw)
+        assert torch.equal(line[at:at + M], want.residual) and torch.equal(line[M:2 * M], r)
+    refused = [(buffer[:, :K], buffer[:, 8:8 + K]), (buffer[:, 8:8 + K], buffer[:, :K])]
+    if M > 1:
+        refused += [(line[1:M + 1], line[:M]), (line[:M], line[1:M + 1]), (buffer[:, :K], buffer.view(-1)[:M * K].view(M, K))]
+    for a, b in refused:
+        with pytest.raises(w8.W8A8Error, match="INVALID_ARG"):
+            w8.block_norm(x, a, residual_out=b, **kw)

@@ -228,3 +228,25 @@ def test_products_refuse_outputs_over_their_inputs(L):
         assert n(a9=at) == m(a10=at) == 1
     # few rows in place need the image of x
     assert n(a4=A, a5=4, a9=None) == m(a4=A, a6=4, a10=None) == n(a4=A, a5=4, a10=image - 1) == m(a4=A, a6=4, a11=100) == 1
+
+
+def test_block_norm_refuses_outputs_that_overlap_its_inputs(L):
+    """Host checks alone: no address is one of memory, and every call is refused."""
+    from w8a8_int8_dynamic_b200.norms import _ARGS
+    M, K, ld = 4, 64, 256
+    X, R, O, Y = (n << 24 for n in range(1, 5))
+
+    def call(x=X, r=R, o=O, y=Y, ldro=K, ldr=K, ldy=K, ldx=K, dtype=1, M=M):
+        return L.w8a8_block_norm(_ARGS.pack(M, K, x, ldx, r, o, ldr, ldro, dtype, 1.0, 0, 0.0, 0, 0, 1, 1e-6, 0, 0, 0, 0, 0,
+                                            0, 0, 0, 0, 0, 0, y, ldy, 0, 0, 0, 0), None)
+
+    rows = M * K * 4                                               # bytes of the fp32 stream
+    for o in (R + 16, R - 16, R + rows - 16, R - rows + 16, X, X + rows // 2 - 16, Y, Y + 16):
+        assert call(o=o) == 1, hex(o)
+    for y in (R, R + rows - 16, X + 16, X - 16, X + rows // 2 - 16, O):
+        assert call(y=y) == 1, hex(y)
+    assert call(o=R, ldro=ld) == call(o=R + K * 4, ldro=ld) == 1    # other strides in one range
+    # columns of one wide tensor: side by side or not
+    for d in (16, K * 4 - 16, -16, ld * 4 - 16, 2 * ld * 4 + 16, -K * 4 + 16):
+        assert call(o=R + d, ldro=ld, ldr=ld) == 1, d
+    assert call(o=R + 16, M=1) == call(o=R - 16, M=1) == 1

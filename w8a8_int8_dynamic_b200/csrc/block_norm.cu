@@ -512,6 +512,30 @@ bool vector_ok(const void *p, int64_t ld, int64_t K, int64_t groups) {
   return !p || ((groups <= 1 || ld == 0 || ld >= K) && ld >= 0);
 }
 
+// Rows of K elements in memory.
+struct Region {
+  uintptr_t at;
+  int64_t stride, width;  // bytes
+  int64_t end(int64_t M) const { return (M - 1) * stride + width; }
+};
+
+Region region(const void *p, int64_t ld, int64_t K, int64_t bytes) {
+  return {reinterpret_cast<uintptr_t>(p), ld * bytes, K * bytes};
+}
+
+// Whether an output may be written while the input is read: the same elements
+// (each is read by the thread that writes it, before it does), or none of
+// them.  Rows of different strides in one range count as overlapping.
+bool apart(const Region &out, const Region &in, int64_t M) {
+  if (!out.at || !in.at) return true;
+  if (out.at >= in.at + in.end(M) || in.at >= out.at + out.end(M)) return true;
+  if (M > 1 && out.stride != in.stride) return false;
+  if (out.at == in.at && out.width == in.width) return true;
+  if (M == 1) return false;
+  const int64_t d = (int64_t)(in.at - out.at) % out.stride, r = d < 0 ? d + out.stride : d;
+  return r >= out.width && out.stride - r >= in.width;  // columns side by side
+}
+
 }  // namespace
 }  // namespace w8a8
 
@@ -636,6 +660,14 @@ extern "C" w8a8_status w8a8_block_norm(const w8a8_block_norm_args *p, w8a8_strea
     if (!four) shape(c, 128);
   }
   if (smem > kMaxFolded) return W8A8_ERR_UNSUPPORTED_SHAPE;
+
+  const int64_t rb = p->residual_dtype == W8A8_DTYPE_FP32 ? 4 : 2;
+  const Region x = region(p->x, p->ldx, K, 2), r = region(p->residual, p->ldr, K, rb);
+  const Region ro = region(p->residual_out, p->ldro, K, rb), y = region(p->y, p->ldy, K, 2);
+  if (!apart(ro, x, M) || !apart(ro, r, M) || !apart(y, x, M) || !apart(y, r, M) ||
+      (ro.at && y.at && (ro.at == y.at || !apart(ro, y, M))))
+    return W8A8_ERR_INVALID_ARG;
+
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)std::min(M, resident));
   cfg.blockDim = dim3((unsigned)(32 * a.W));

@@ -82,7 +82,7 @@ def block_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, *, post
 
     x: bf16 [..., K], the block's output (without ``residual``: what ``pre`` norms).
     residual: bf16 or fp32 [..., K]; the new stream goes to ``residual_out`` (``residual`` itself
-    for an update in place) or to a new tensor.
+    for an update in place; other memory that overlaps neither it nor x) or to a new tensor.
     gate, scale, shift: bf16 [groups, K] (slices of a wider tensor may be given as they are; [K]
     for one group).  The group of row m is ``group_index[m]`` (int32; a row whose index is
     outside the groups, or negative where none of the three is given, is padding and is left alone),
