@@ -85,7 +85,8 @@ def block_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, *, post
     for an update in place; other memory that overlaps neither it nor x) or to a new tensor.
     gate, scale, shift: bf16 [groups, K] (slices of a wider tensor may be given as they are; [K]
     for one group).  The group of row m is ``group_index[m]`` (int32; a row whose index is
-    outside the groups, or negative where none of the three is given, is padding and is left alone),
+    outside the groups, or negative where none of the three is given, is padding: not computed, its
+    part of ``residual_out`` left as it was, of the new tensors undefined),
     else m // ``rows_per_group``; one of the two has to be given where there are several groups
     (a single one takes all rows).
     codes: "int8" (``q`` and ``a_scale``, for ``W8A8Linear.apply_codes``) or "mx4" (an ``MX4Tensor``, for
