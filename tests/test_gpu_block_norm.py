@@ -358,3 +358,16 @@ def test_the_stream_over_its_inputs(M):
     for a, b in refused:
         with pytest.raises(w8.W8A8Error, match="INVALID_ARG"):
             w8.block_norm(x, a, residual_out=b, **kw)
+
+
+def test_int8_codes_of_rows_at_the_ends_of_the_range():
+    """Codes and scales of the output as quant_act forms them, bit for bit: NaN and infinite rows, zeros, scales below 1e-30."""
+    x, _, _, (w, b), _ = tensors(37, 8, 1040)
+    x[1, 3], x[2, 5], x[3] = float("nan"), float("inf"), 0
+    x[4] *= 2.0 ** -40
+    x[5] *= 2.0 ** -100
+    for kw in (dict(pre=w8.Norm("rms", w, eps=1e-2)), dict(pre=w8.Norm("layer", w, b)),
+               dict(pre=w8.Norm("rms", (w.double() * 2.0 ** -110).bfloat16())), dict(pre=w8.Norm("rms", w * 1e30))):
+        out = w8.block_norm(x, y=True, codes="int8", **kw)
+        q, s = w8.quant_act(out.y)
+        assert torch.equal(out.q, q) and torch.equal(out.a_scale.view(torch.int32), s.view(torch.int32))

@@ -1,5 +1,7 @@
 """GPU tests of the 4-bit layers and the block norm as a serving program runs them: together, on other streams, in
 CUDA graphs, back to back, in place, with rows or values left out, and on tensors longer than 32-bit offsets reach."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -389,3 +391,42 @@ def test_a_wide_layer_over_its_input(M):
         buffer = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")
         v = buffer.view(-1)[:M * K].view(M, K).copy_(x)
         assert torch.equal(w8.mx4_linear(v, w, b, out=buffer), want)
+
+
+def test_calls_from_several_host_threads():
+    """Four threads, each on a stream of its own, with layers, norms and codes that they share: every result is that of
+    one thread, the first calls of each shape among them."""
+    D, F = 656, 1296
+    up, down, n, mod = layers(13, D, F)
+    eight = w8.W8A8Linear.from_float(up.w.dequant())
+    xs = [sample(np.random.default_rng(M), M, D) for M in (1, 9, 16, 18, 33, 70, 129, 400)]
+    torch.cuda.synchronize()
+
+    def work(x):
+        out = block(x, x.float(), up, down, n, mod, -(-x.shape[0] // 2))
+        q = w8.block_norm(x, pre=n, codes="int8")
+        return out.residual, out.y, eight.apply_codes(q.q, q.a_scale), w8.mx4_quant(x).dequant()
+
+    got, failed = {}, []
+
+    def run(i):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for r in range(12):
+                    k = (i * 3 + r) % len(xs)
+                    got[i, r] = (k, work(xs[k]))
+            s.synchronize()
+        except BaseException as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    want = [work(x) for x in xs]
+    torch.cuda.synchronize()
+    for k, outs in got.values():
+        assert all(torch.equal(g, v) for g, v in zip(outs, want[k]))
