@@ -371,3 +371,21 @@ def test_int8_codes_of_rows_at_the_ends_of_the_range():
         out = w8.block_norm(x, y=True, codes="int8", **kw)
         q, s = w8.quant_act(out.y)
         assert torch.equal(out.q, q) and torch.equal(out.a_scale.view(torch.int32), s.view(torch.int32))
+
+
+@pytest.mark.parametrize("codes", ["int8", "mx4"])
+def test_outputs_of_one_row_of_a_wider_tensor(codes):
+    """A lone row's stride may be any, and its tensor still counts as contiguous: the outputs' strides are those of dense
+    rows, which the next call takes."""
+    K = 272
+    x, r, _, (w, _), _ = tensors(41, 1, K)
+    want = w8.block_norm(x, r, pre=w8.Norm("rms", w), codes=codes, y=True)
+    for width in (276, 299, 400):
+        wx, wr = (torch.zeros(1, width, dtype=t.dtype, device="cuda")[:, :K].copy_(t) for t in (x, r))
+        assert wx.stride() == (width, 1)
+        got = w8.block_norm(wx, wr, pre=w8.Norm("rms", w), codes=codes, y=True)
+        for g, v in zip((got.residual, got.y, got.q), (want.residual, want.y, want.q)):
+            assert v is None or g.stride() == (K, 1) and torch.equal(g, v)
+        q, s = w8.quant_act(got.y)
+        if codes == "int8":
+            assert torch.equal(q, got.q) and torch.equal(s, got.a_scale)

@@ -6,7 +6,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from .binding import _bytes, _check, _device, _elsewhere, _need_cuda, _new, _raw_stream, _rows_of, _there, lib
+from .binding import _bytes, _check, _device, _elsewhere, _need_cuda, _raw_stream, _rows_of, _there, lib
 from .mx4 import MX4Tensor, mx4_bytes
 
 _KINDS = {"rms": 1, "layer": 2}
@@ -125,14 +125,14 @@ def block_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, *, post
                               scale=scale, shift=shift, rows_per_group=rows_per_group,
                               group_index=group_index, codes=codes, y=y, residual_out=residual_out)
     x2, M, ldx = _rows_of(x)
-    plain = x.is_contiguous()  # outputs of its strides are the dense ones that the kernel writes
+    dense = torch.contiguous_format  # (a single row's stride may be any; the outputs' are those of dense rows)
     r2 = new = None
     ldr = ldro = dtype = 0
     if residual is not None:
         r2, _, ldr = _rows_of(residual)
         dtype, ldro = _RESIDUAL[residual.dtype], K
         if residual_out is None:
-            new = torch.empty_like(residual) if residual.is_contiguous() else _new(x.shape[:-1], K, r2.dtype, index)
+            new = torch.empty_like(residual, memory_format=dense)
         else:  # written in place: a view, never a copy
             new = residual_out
             n2 = new.view(-1, K) if new.is_contiguous() else new
@@ -162,9 +162,9 @@ def block_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, *, post
 
     out = q = a_scale = image = None
     if want_y:
-        out = torch.empty_like(x) if plain else _new(x.shape[:-1], K, torch.bfloat16, index)
+        out = torch.empty_like(x, memory_format=dense)
     if codes == "int8":
-        q = torch.empty_like(x, dtype=torch.int8) if plain else _new(x.shape[:-1], K, torch.int8, index)
+        q = torch.empty_like(x, dtype=torch.int8, memory_format=dense)
         a_scale = torch.empty_strided((M,), (1,), dtype=torch.float32, device=index)
     elif codes == "mx4":
         image = _bytes(mx4_bytes(M, K) if M else 0, index)
