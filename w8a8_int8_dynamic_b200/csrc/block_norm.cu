@@ -627,7 +627,7 @@ extern "C" w8a8_status w8a8_block_norm(const w8a8_block_norm_args *p, w8a8_strea
   // quarter of the warps is lost: a row takes longer, but fewer instructions
   // (8192 x 4096 59 us, with two chunks 67; 1000 x 4096 13.9 and 13.0; 4096 x
   // 4096 with an fp32 residual 44.1 and 43.1; 4096 x 8192, half the warps, 77
-  // and 68).  Past 8192 three, where they suffice (4000 x 10240, fp32 residual,
+  // and 69).  Past 8192 three, where they suffice (4000 x 10240, fp32 residual,
   // 116 us; with four 175).  The outputs have no say: y has the same bits
   // beside codes or alone.  (An image's padding columns, to 256, are always
   // within the warps' parts, whose lanes there write them.)
