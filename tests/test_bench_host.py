@@ -3,6 +3,7 @@ replays, how many rotated input sets a workload needs to exceed L2, and when
 the recorded DRAM traffic of the dominant kernel still applies."""
 import hashlib
 import json
+import os
 
 import pytest
 
@@ -188,3 +189,10 @@ def test_sweep_loops_hold_about_25_ms_of_work():
     # the 4096-token MLP layers are the longest: a few hundred steps at most
     assert rows["dit_mlp_up_4096x12288x3072"] < 300
     assert rows["small_64x128x256"] == 2000
+
+
+def test_the_recorded_traffic_is_of_the_sources_as_they_are():
+    """A record whose sources have changed since its capture reads as none, and the bench then reports no traffic."""
+    with open(os.path.join(bench.HERE, "profiles", "traffic.json")) as f:
+        records = [n for n in json.load(f) if not n.startswith("_")]
+    assert records and all(bench.recorded_traffic(n) for n in records)

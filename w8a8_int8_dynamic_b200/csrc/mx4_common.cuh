@@ -29,6 +29,27 @@
 
 namespace w8a8 {
 
+// One lane of a converged warp (the same one on every call).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// 16 bytes that are read once, through the coherent path: for what the kernel
+// ahead in the stream may have written after this one started (the read-only
+// path is for memory that nothing writes while the kernel runs).
+__device__ __forceinline__ uint4 ld_once_u4(const void *p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
 constexpr int kMxTileRows = 128;
 constexpr int kMxTileK = 256;                // elements: 128 bytes of codes a row
 constexpr int kMxCodeBytes = 128 * 128;      // 16 KB
